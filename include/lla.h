@@ -64,6 +64,9 @@ extern "C" {
 #define LLA_STATUS_CTX_RANGE 2      /* ctx_len[b] outside [0, n_cap] (clamped) */
 #define LLA_STATUS_SLOT_RANGE 4     /* an encode slot outside [0, n_slots) (skipped) */
 #define LLA_STATUS_TIMEOUT 8        /* a kernel wait timed out; that call's output is invalid */
+#define LLA_STATUS_PAGE_RANGE 16    /* a page outside [0, n_pages), or a free list out of bounds */
+#define LLA_STATUS_PAGES_SHORT 32   /* lla_page_map: a sequence was not served */
+#define LLA_STATUS_NONFINITE 64     /* lla_q8_append: a NaN or an infinity among keys or values */
 
 /*
  * Codec geometry of one shared layer.
@@ -94,7 +97,7 @@ typedef struct lla_cfg {
 const char* lla_last_error(void);
 
 /* Library version string ("lla-b200 <major>.<minor> ..."); 0.2 added lla_cfg.d_rope,
- * the full-memory fast path and the eviction calls. */
+ * the full-memory fast path and the eviction calls; 0.3 the rotary, page and 8-bit cache calls. */
 const char* lla_version(void);
 
 /* ------------------------------------------------------------------------ */
@@ -360,6 +363,193 @@ int lla_full_decode_attn(const lla_cfg* cfg, const void* rope_table, int32_t rop
                          const float* k_self, const float* v_self, const int32_t* q_pos,
                          const uint16_t* k_full, const uint16_t* v_full, float* out, void* ws,
                          size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions as operators.                                             */
+/* ------------------------------------------------------------------------ */
+
+#define LLA_ROPE_HALF 0        /* pairs (i, i + rd/2) */
+#define LLA_ROPE_INTERLEAVED 1 /* pairs (2i, 2i + 1) */
+
+#define LLA_F32 0
+#define LLA_BF16 1
+
+/*
+ * Frequencies for contexts longer than the trained one.  With theta_i =
+ * rope_base^(-2i/rd), rd the rotary dims (d_rope, or d_head when d_rope is 0), and
+ * s = factor (>= 1), position p turns pair i by p times
+ *   NONE    theta_i
+ *   LINEAR  theta_i / s
+ *   NTK     (rope_base * s^(rd/(rd-2)))^(-2i/rd)
+ *   YARN    theta_i (1 - r_i) + theta_i / s * r_i, with the ramp r_i rising from 0 at
+ *           pair max(floor(at(beta_fast)), 0) to 1 at min(ceil(at(beta_slow)), rd - 1),
+ *           at(n) = rd ln(orig_len / (2 pi n)) / (2 ln rope_base), the pair that turns n
+ *           times over the orig_len positions trained on.
+ * The tables stay plain rotations: the attention factor that goes with YARN
+ * ((0.1 ln s + 1)^2 on the scores of whole-head RoPE) belongs in lla_cfg.sm_scale.
+ */
+#define LLA_ROPE_SCALE_NONE 0
+#define LLA_ROPE_SCALE_LINEAR 1
+#define LLA_ROPE_SCALE_NTK 2
+#define LLA_ROPE_SCALE_YARN 3
+
+typedef struct lla_rope_scaling {
+  int32_t kind;      /* LLA_ROPE_SCALE_* */
+  int32_t orig_len;  /* YARN: trained context, >= 1 */
+  double factor;     /* s, finite and >= 1 */
+  double beta_fast;  /* YARN; 0 selects 32 */
+  double beta_slow;  /* YARN; 0 selects 1; below beta_fast */
+} lla_rope_scaling;
+
+/*
+ * lla_rope_table with scaled frequencies (same layout, size and accuracy).  Such a
+ * table serves lla_rope_apply, the lla_q8_* and the lla_full_* calls, which take their
+ * angles from it.  lla_decode_attn does not: its kernels form angles from rope_base.
+ */
+int lla_rope_table_scaled(const lla_cfg* cfg, const lla_rope_scaling* scaling, int32_t max_pos,
+                          void* table, size_t table_bytes, void* stream);
+
+/*
+ * y = x rotated at its positions, on rows of n_heads heads of d_head:
+ *   (y_a, y_b) = (x_a c - x_b s, x_a s + x_b c) on the pairs (a, b) of `layout` among the
+ *   rotary dims, (c, s) the table's row at positions[token]; other dims are copied.
+ * inverse != 0 rotates back, which is also the gradient: dL/dx = inverse rotation of dL/dy.
+ *   x, y       device, dtype LLA_F32 or LLA_BF16 (arithmetic in fp32): token i's heads
+ *              start at element i * stride and are contiguous; strides in elements, whole
+ *              multiples of 16 bytes, at least n_heads * d_head.  y == x with the same
+ *              stride rotates in place; rows of x and y must not overlap otherwise
+ *              (LLA_ERR_INVALID), but may alternate in one buffer with one stride.
+ *   positions  device int32 [n_tok]; outside [0, rope_max_pos) they are clamped and
+ *              LLA_STATUS_POSITION_RANGE is OR-ed into status (device int32, may be NULL).
+ * 1 <= n_heads <= 4096; n_tok == 0 is a no-op.
+ */
+int lla_rope_apply(const lla_cfg* cfg, const void* rope_table, int32_t rope_max_pos,
+                   int32_t layout, int32_t inverse, int32_t dtype, int64_t n_tok,
+                   int32_t n_heads, const int32_t* positions, const void* x, int64_t x_stride,
+                   void* y, int64_t y_stride, int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Pages: block tables and slot maps from request lengths.                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A paged cache keeps sequence b's token j in row j % page of page
+ * block_table[b][j / page].  One call grows and shrinks every sequence of a batch:
+ *   n_new      device int32 [B]: n_new[b] > 0 appends that many tokens, < 0 drops the last
+ *              -n_new[b] (all of them when it holds fewer), 0 leaves the sequence.
+ *   ctx_len    device int32 [B] (in/out): the lengths.
+ *   block_table device int32 [B][max_pages] (in/out): entries [0, ceil(len/page)) are the
+ *              sequence's pages; entries given back become -1, others are not touched.
+ *   free_list  device int32 [n_pages] (in/out), n_free device int32 [1] (in/out): the pages
+ *              free_list[0 .. n_free) are free; the top is taken first.
+ *   tok_start  device int32 [B + 1] (out): the appended tokens of sequence b are tokens
+ *              tok_start[b] .. tok_start[b + 1] of the batch (prefix sums).
+ *   slot       device int64 [tok_cap] (out): each token's row page_id * page + offset in the
+ *              cache; -1 past the last token.  positions device int32 [tok_cap] (out): its
+ *              index in its sequence; 0 past the last token.
+ * Pages given back are free for the same call.  Growing sequences are served in order:
+ * one whose pages, with all that was asked before it, exceed the free ones, or whose
+ * tokens likewise exceed tok_cap, is left as it was (LLA_STATUS_PAGES_SHORT), and so is
+ * one that would pass max_pages * page tokens or whose ctx_len is outside that range
+ * (LLA_STATUS_CTX_RANGE).  Dropping the tokens a call just appended restores free_list,
+ * n_free, ctx_len and block_table (whose new entries become -1).  A page index outside
+ * [0, n_pages) is kept as -1 and sets LLA_STATUS_PAGE_RANGE; tokens in it get slot -1.
+ * page in {16, 32, 64, 128}; B <= 65535; max_pages * page and tok_cap below 2^31.  slot and
+ * positions may be NULL when tok_cap == 0.  Pointers 4-byte (slot 8-byte) aligned; status
+ * (device int32, may be NULL) collects the bits.  No buffer may overlap another.
+ */
+int lla_page_map(int32_t B, int32_t page, int32_t max_pages, int32_t n_pages, int32_t* ctx_len,
+                 const int32_t* n_new, int32_t* block_table, int32_t* free_list, int32_t* n_free,
+                 int64_t tok_cap, int32_t* tok_start, int64_t* slot, int32_t* positions,
+                 int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Paged 8-bit cache: exact keys and values, one scale per page and head.     */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The 8-bit cache keeps a token's own keys and values of one loop and layer (close
+ * reading §三.2's kv_quant, without the latent codec) in int8, value = code * scale:
+ *   k, v             device int8 [n_pages][H][page][d_head]; keys are stored rotated
+ *   k_scale, v_scale device fp32 [n_pages][H]
+ * half the bytes of the lla_full cache, in pages that sequences of any length share.
+ * The cfg's codec fields (T, r_k, r_v, mode) are not used; H, d_head, d_rope, rope_base
+ * and sm_scale are.  A value is off by at most half its page's scale per rounding.
+ */
+typedef struct lla_q8_cache {
+  int8_t* k;
+  int8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t n_pages;
+  int32_t page;      /* tokens per page: 16, 32, 64 or 128 */
+} lla_q8_cache;
+
+/* Bytes of k (or of v) for n_pages pages; 0 if the arguments are invalid. */
+size_t lla_q8_cache_bytes(const lla_cfg* cfg, int32_t n_pages, int32_t page);
+
+/*
+ * Append tokens: tokens tok_start[b] .. tok_start[b + 1] of k and v are the last ones of
+ * sequence b, whose length with them is ctx_len[b] (as lla_page_map leaves them).
+ *   k, v       dtype LLA_F32 or LLA_BF16, rows of H heads of d_head, k_stride / v_stride
+ *              elements apart (as lla_rope_apply's); n_tok rows are there to read.
+ *   rope_table, rope_max_pos, layout, positions [n_tok]: keys are rotated in fp32 on the way,
+ *              as by lla_rope_apply.  rope_table NULL: keys come rotated, positions unused.
+ * Per page and head, with amax the largest magnitude among the new tokens' values:
+ *   page without earlier tokens   scale = amax / 127
+ *   page with earlier tokens      scale kept if amax / 127 <= scale, else it becomes
+ *                                 max(amax / 127, 1.25 scale) and the codes of the earlier
+ *                                 tokens are rounded again; later rows are not touched
+ *   code = round(value / scale), ties to even.
+ * An amax of 1e-30 or less stores zeros.  NaN is stored as 0 and an infinity as the
+ * largest code (amax looks at finite values), with LLA_STATUS_NONFINITE.  A page must
+ * belong to one appended sequence only: written from two, its contents are unspecified.
+ * Sequences whose tok_start or ctx_len do not fit (LLA_STATUS_CTX_RANGE) and pages
+ * outside the cache (LLA_STATUS_PAGE_RANGE) are skipped.  B <= 65535.
+ */
+int lla_q8_append(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
+                  int32_t rope_max_pos, int32_t layout, int32_t dtype, int32_t B,
+                  int32_t max_pages, const int32_t* ctx_len, const int32_t* block_table,
+                  int32_t n_tok, const int32_t* tok_start, const int32_t* positions,
+                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                  int32_t* status, void* stream);
+
+/*
+ * Rows of the cache as bf16: k_out, v_out [n_rows][H][d_head] = code * scale of row slot[i]
+ * (page_id * page + offset, as lla_page_map's slots).  A slot outside the cache leaves its
+ * output row as it was (LLA_STATUS_SLOT_RANGE).
+ */
+int lla_q8_read(const lla_cfg* cfg, const lla_q8_cache* cache, int64_t n_rows,
+                const int64_t* slot, uint16_t* k_out, uint16_t* v_out, int32_t* status,
+                void* stream);
+
+/* Workspace bytes of lla_q8_decode_attn for sequences of up to n_cap tokens (zero-filled
+ * once before first use; its first two int32 words are the status words described at
+ * lla_decode_workspace_bytes); 0 if the arguments are invalid. */
+size_t lla_q8_decode_workspace_bytes(const lla_cfg* cfg, int32_t B, int32_t n_cap);
+
+/* Kernel launches one lla_q8_decode_attn call makes, or -1 if invalid. */
+int lla_q8_decode_launches(const lla_cfg* cfg, int32_t B, int32_t n_cap);
+
+/*
+ * Decode attention, one token per sequence, over the 8-bit cache and the in-flight token:
+ *   s_j    = sm_scale * RoPE(q, q_pos[b]) . k_j (j < ctx_len[b]),  s_self likewise
+ *   out    = sum_j p_j v_j + p_self v_self,  p = softmax(s, s_self)
+ *   q, k_self, v_self, out   dtype [B][H][d_head]; k_self and v_self both NULL: the history
+ *              alone (a sequence of length 0 then gives zeros)
+ *   ctx_len [B], block_table [B][max_pages], q_pos [B] device int32 (q_pos unused and
+ *              rope_table NULL when q and k_self come rotated)
+ *   ws         >= lla_q8_decode_workspace_bytes(cfg, B, max_pages * page)
+ * Tokens of a page outside the cache are left out (LLA_STATUS_PAGE_RANGE); what the cache
+ * holds past ctx_len[b] or in pages of other sequences does not reach the output.
+ * Scores, softmax and sums are held in fp32 or exact integers.
+ */
+int lla_q8_decode_attn(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
+                       int32_t rope_max_pos, int32_t layout, int32_t dtype, int32_t B,
+                       int32_t max_pages, const int32_t* ctx_len, const int32_t* block_table,
+                       const void* q, const void* k_self, const void* v_self,
+                       const int32_t* q_pos, void* out, void* ws, size_t ws_bytes,
+                       void* stream);
 
 #ifdef __cplusplus
 }

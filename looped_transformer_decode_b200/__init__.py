@@ -7,13 +7,16 @@ library's CUDA kernels.  Tensors must be contiguous CUDA tensors.
 from __future__ import annotations
 
 import ctypes
+from dataclasses import dataclass
 from fractions import Fraction
 
 import torch
 
-from ._lib import (ERR_CUDA, ERR_INVALID, ERR_TOO_SMALL, ERR_UNSUPPORTED, LIB_PATH, MODE_2D,
-                   MODE_PER_HEAD, OK, SIGNATURES, STATUS_CTX_RANGE, STATUS_POSITION_RANGE,
-                   STATUS_SLOT_RANGE, Cfg, LLAError, check, last_error, lib)
+from ._lib import (BF16, ERR_CUDA, ERR_INVALID, ERR_TOO_SMALL, ERR_UNSUPPORTED, F32, LIB_PATH,
+                   MODE_2D, MODE_PER_HEAD, OK, ROPE_LAYOUTS, SIGNATURES, STATUS_CTX_RANGE,
+                   STATUS_NONFINITE, STATUS_PAGE_RANGE, STATUS_PAGES_SHORT, STATUS_POSITION_RANGE,
+                   STATUS_SLOT_RANGE, STATUS_TIMEOUT, Cfg, CQ8Cache, LLAError, RopeScaling, check,
+                   last_error, lib)
 
 __all__ = [
     "Cfg", "LLAError", "MODE_PER_HEAD", "MODE_2D", "ratio", "cache_bytes", "codec_pack",
@@ -21,6 +24,9 @@ __all__ = [
     "decode_launches", "STATUS_POSITION_RANGE", "STATUS_CTX_RANGE", "STATUS_SLOT_RANGE",
     "evict_slot", "evict_append", "full_kv_bytes", "full_cache_alloc", "full_rebuild",
     "full_decode_workspace", "full_decode_launches", "full_decode_attn",
+    "RopeScaling", "rope_apply", "page_map", "Q8Cache", "q8_cache_alloc", "q8_append", "q8_read",
+    "q8_decode_workspace", "q8_decode_launches", "q8_decode_attn", "STATUS_TIMEOUT",
+    "STATUS_PAGE_RANGE", "STATUS_PAGES_SHORT", "STATUS_NONFINITE",
 ]
 
 
@@ -80,11 +86,19 @@ def codec_pack(cfg: Cfg, W_down_k, W_down_v, W_up_k, W_up_v, mu_k, mu_v, out=Non
     return out
 
 
-def rope_table(cfg: Cfg, max_pos: int, device="cuda", out=None):
+def rope_table(cfg: Cfg, max_pos: int, device="cuda", out=None, scaling: RopeScaling | None = None):
+    """(cos, sin) rows [max_pos, rd / 2, 2].  ``scaling`` stretches the context (for rope_apply,
+    the q8 and the full-memory calls; decode_attn forms its angles from ``rope_base``)."""
     c = cfg.c()
     if out is None:
         rd = cfg.d_rope or cfg.d_head                 # rotary dims
         out = torch.empty((max_pos, rd // 2, 2), dtype=torch.float32, device=device)
+    if scaling is not None:
+        with torch.cuda.device(out.device):
+            check(lib.lla_rope_table_scaled(ctypes.byref(c), ctypes.byref(scaling.c()), max_pos,
+                                            _ptr(out, torch.float32, "table"), out.numel() * 4,
+                                            _stream()))
+        return out
     check(lib.lla_rope_table(ctypes.byref(c), max_pos, _ptr(out, torch.float32, "table"),
                              out.numel() * 4, _stream()))
     return out
@@ -248,4 +262,241 @@ def full_decode_attn(cfg: Cfg, rope, ctx_len, q, k_self, v_self, q_pos, k_full, 
         _ptr(k_full, torch.bfloat16, "k_full", fs), _ptr(v_full, torch.bfloat16, "v_full", fs),
         _ptr(out, torch.float32, "out", (B, H, d)), _ptr(ws, torch.uint8, "ws"), ws.numel(),
         _stream()))
+    return out
+
+
+# ---------------------------------------------------------------- rotary positions
+
+_ROW_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _layout(layout: str) -> int:
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout {layout!r} not in {sorted(ROPE_LAYOUTS)}")
+    return ROPE_LAYOUTS[layout]
+
+
+def _same_device(first: torch.Tensor, **others):
+    """Device context of ``first``; every other tensor (None skipped) must live there too."""
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    for name, t in others.items():
+        if isinstance(t, torch.Tensor) and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    return torch.cuda.device(first.device)
+
+
+def _opt(t, dtype, name, shape=None):
+    return None if t is None else _ptr(t, dtype, name, shape)
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, name: str, shape):
+    """Pointer and token stride of rows [n, heads, d] whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, heads, d = t.shape
+    if n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    stride = t.stride(0) if n > 1 else heads * d
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def _check_table(cfg: Cfg, rope) -> int:
+    """Positions covered by a rope table, whose rows must be cfg's; 0 without one."""
+    if rope is None:
+        return 0
+    rd = cfg.d_rope or cfg.d_head
+    if rope.dim() != 3 or tuple(rope.shape[1:]) != (rd // 2, 2):
+        raise ValueError(f"rope has shape {tuple(rope.shape)}, expected (positions, {rd // 2}, 2)")
+    return rope.shape[0]
+
+
+def _row_type(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or t.dtype not in _ROW_TYPES:
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+    return _ROW_TYPES[t.dtype]
+
+
+def rope_apply(cfg: Cfg, rope, positions, x, layout: str = "half", inverse: bool = False, out=None,
+               status=None):
+    """Rotate rows x [n_tok, heads, d] (fp32 or bf16) at ``positions`` int32 [n_tok].
+
+    Rotary dims as ``cfg`` has them, pairs by ``layout`` ("half" or "interleaved").  Tokens may be
+    strided (a slice of a fused projection); ``out`` may be ``x``.  ``inverse=True`` rotates back,
+    which is the gradient with respect to x given the gradient of the output.
+    """
+    kind = _row_type(x, "x")
+    if x.dim() != 3 or x.shape[2] != cfg.d_head:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected (tokens, heads, {cfg.d_head})")
+    n, heads, _ = x.shape
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    with _same_device(x, rope=rope, positions=positions, out=out, status=status):
+        xp, xs = _rows(x, x.dtype, "x", x.shape)
+        yp, ys = _rows(out, x.dtype, "out", x.shape)
+        check(lib.lla_rope_apply(ctypes.byref(cfg.c()), _ptr(rope, torch.float32, "rope"),
+                                 _check_table(cfg, rope), _layout(layout), int(inverse), kind, n,
+                                 heads, _ptr(positions, torch.int32, "positions", (n,)), xp, xs,
+                                 yp, ys, _opt(status, torch.int32, "status"), _stream()))
+    return out
+
+
+# ---------------------------------------------------------------- pages
+
+def page_map(page: int, ctx_len, n_new, block_table, free_list, n_free, tok_cap: int,
+             tok_start=None, slot=None, positions=None, status=None):
+    """Grow (or shrink) every sequence by ``n_new`` int32 [B] tokens; see ``lla_page_map``.
+
+    Updates ``ctx_len`` [B], ``block_table`` [B, max_pages], ``free_list`` [n_pages] and
+    ``n_free`` [1] (all int32) in place.  Returns (tok_start int32 [B + 1], slot int64 [tok_cap],
+    positions int32 [tok_cap]) of the appended tokens.
+    """
+    if block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("block_table must be [B, max_pages] and free_list [n_pages]")
+    B, max_pages = block_table.shape
+    dev = ctx_len.device
+    if tok_start is None:
+        tok_start = torch.empty((B + 1,), dtype=torch.int32, device=dev)
+    if slot is None:
+        slot = torch.empty((tok_cap,), dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty((tok_cap,), dtype=torch.int32, device=dev)
+    i32 = torch.int32
+    with _same_device(ctx_len, n_new=n_new, block_table=block_table, free_list=free_list,
+                      n_free=n_free, tok_start=tok_start, slot=slot, positions=positions,
+                      status=status):
+        check(lib.lla_page_map(
+            B, page, max_pages, free_list.shape[0], _ptr(ctx_len, i32, "ctx_len", (B,)),
+            _ptr(n_new, i32, "n_new", (B,)), _ptr(block_table, i32, "block_table"),
+            _ptr(free_list, i32, "free_list"), _ptr(n_free, i32, "n_free", (1,)), tok_cap,
+            _ptr(tok_start, i32, "tok_start", (B + 1,)),
+            _ptr(slot, torch.int64, "slot", (tok_cap,)),
+            _ptr(positions, i32, "positions", (tok_cap,)), _opt(status, i32, "status"), _stream()))
+    return tok_start, slot, positions
+
+
+# ---------------------------------------------------------------- paged 8-bit cache
+
+@dataclass
+class Q8Cache:
+    """Paged 8-bit cache: int8 k, v [n_pages, H, page, d], fp32 k_scale, v_scale [n_pages, H]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @property
+    def page(self) -> int:
+        return self.k.shape[2]
+
+    @property
+    def n_pages(self) -> int:
+        return self.k.shape[0]
+
+    def c(self, cfg: Cfg) -> CQ8Cache:
+        n, page = self.n_pages, self.page
+        shape, rows = (n, cfg.H, page, cfg.d_head), (n, cfg.H)
+        return CQ8Cache(_ptr(self.k, torch.int8, "cache.k", shape),
+                        _ptr(self.v, torch.int8, "cache.v", shape),
+                        _ptr(self.k_scale, torch.float32, "cache.k_scale", rows),
+                        _ptr(self.v_scale, torch.float32, "cache.v_scale", rows), n, page)
+
+
+def q8_cache_alloc(cfg: Cfg, n_pages: int, page: int, device="cuda") -> Q8Cache:
+    """Empty 8-bit cache of ``n_pages`` pages of ``page`` tokens (16, 32, 64 or 128)."""
+    shape = (n_pages, cfg.H, page, cfg.d_head)
+    return Q8Cache(torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+
+def q8_append(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, tok_start, positions, k, v,
+              layout: str = "half", status=None):
+    """Quantise new tokens' keys and values into the cache's pages (see ``lla_q8_append``).
+
+    ``k``, ``v`` fp32 or bf16 [n_tok, H, d], tokens possibly strided; ``ctx_len`` and
+    ``tok_start`` as ``page_map`` leaves them.  Keys are rotated by ``rope`` at ``positions`` int32
+    [n_tok]; with ``rope=None`` (then ``positions`` may be None) they come rotated.
+    """
+    kind = _row_type(k, "k")
+    n, B, max_pages = k.shape[0], block_table.shape[0], block_table.shape[1]
+    i32 = torch.int32
+    with _same_device(k, rope=rope, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
+                      v_scale=cache.v_scale, ctx_len=ctx_len, block_table=block_table,
+                      tok_start=tok_start, positions=positions, v=v, status=status):
+        kp, ks = _rows(k, k.dtype, "k", (n, cfg.H, cfg.d_head))
+        vp, vs = _rows(v, k.dtype, "v", (n, cfg.H, cfg.d_head))
+        check(lib.lla_q8_append(
+            ctypes.byref(cfg.c()), ctypes.byref(cache.c(cfg)), _opt(rope, torch.float32, "rope"),
+            _check_table(cfg, rope), _layout(layout), kind, B, max_pages,
+            _ptr(ctx_len, i32, "ctx_len", (B,)), _ptr(block_table, i32, "block_table"), n,
+            _ptr(tok_start, i32, "tok_start", (B + 1,)),
+            _opt(positions, i32, "positions", (n,)), kp, ks, vp, vs,
+            _opt(status, i32, "status"), _stream()))
+
+
+def q8_read(cfg: Cfg, cache: Q8Cache, slot, k_out=None, v_out=None, status=None):
+    """Rows ``slot`` int64 [n] (page * page_size + offset) of the cache as bf16 [n, H, d] each.
+
+    A slot outside the cache leaves its row as it was (zeros without ``k_out`` / ``v_out``).
+    """
+    shape = (slot.shape[0], cfg.H, cfg.d_head)
+    bf = torch.bfloat16
+    if k_out is None:
+        k_out = torch.zeros(shape, dtype=bf, device=slot.device)
+    if v_out is None:
+        v_out = torch.zeros(shape, dtype=bf, device=slot.device)
+    with _same_device(slot, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
+                      v_scale=cache.v_scale, k_out=k_out, v_out=v_out, status=status):
+        check(lib.lla_q8_read(ctypes.byref(cfg.c()), ctypes.byref(cache.c(cfg)), shape[0],
+                              _ptr(slot, torch.int64, "slot", shape[:1]),
+                              _ptr(k_out, bf, "k_out", shape), _ptr(v_out, bf, "v_out", shape),
+                              _opt(status, torch.int32, "status"), _stream()))
+    return k_out, v_out
+
+
+def q8_decode_workspace(cfg: Cfg, B: int, n_cap: int, device="cuda"):
+    """Workspace of q8_decode_attn for sequences of up to ``n_cap`` = max_pages * page tokens."""
+    n = lib.lla_q8_decode_workspace_bytes(ctypes.byref(cfg.c()), B, n_cap)
+    if n == 0:
+        raise LLAError(ERR_UNSUPPORTED, last_error())
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def q8_decode_launches(cfg: Cfg, B: int, n_cap: int) -> int:
+    return lib.lla_q8_decode_launches(ctypes.byref(cfg.c()), B, n_cap)
+
+
+def q8_decode_attn(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, q, k_self, v_self, q_pos,
+                   layout: str = "half", out=None, ws=None):
+    """Decode attention over the 8-bit cache; returns out [B, H, d] of q's dtype.
+
+    ``q``, ``k_self``, ``v_self`` fp32 or bf16 [B, H, d] before rotation (rotated already with
+    ``rope=None``); ``k_self=v_self=None`` attends over the history alone.
+    """
+    kind = _row_type(q, "q")
+    B, max_pages = block_table.shape
+    rows = (B, cfg.H, cfg.d_head)
+    if out is None:
+        out = torch.empty(rows, dtype=q.dtype, device=q.device)
+    if ws is None:
+        ws = q8_decode_workspace(cfg, B, max_pages * cache.page, q.device)
+    i32 = torch.int32
+    with _same_device(q, rope=rope, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
+                      v_scale=cache.v_scale, ctx_len=ctx_len, block_table=block_table,
+                      k_self=k_self, v_self=v_self, q_pos=q_pos, out=out, ws=ws):
+        check(lib.lla_q8_decode_attn(
+            ctypes.byref(cfg.c()), ctypes.byref(cache.c(cfg)), _opt(rope, torch.float32, "rope"),
+            _check_table(cfg, rope), _layout(layout), kind, B, max_pages,
+            _ptr(ctx_len, i32, "ctx_len", (B,)), _ptr(block_table, i32, "block_table"),
+            _ptr(q, q.dtype, "q", rows), _opt(k_self, q.dtype, "k_self", rows),
+            _opt(v_self, q.dtype, "v_self", rows), _opt(q_pos, i32, "q_pos", (B,)),
+            _ptr(out, q.dtype, "out", rows), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()))
     return out

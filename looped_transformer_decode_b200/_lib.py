@@ -19,6 +19,14 @@ MODE_2D = 1
 STATUS_POSITION_RANGE = 1
 STATUS_CTX_RANGE = 2
 STATUS_SLOT_RANGE = 4
+STATUS_TIMEOUT = 8
+STATUS_PAGE_RANGE = 16
+STATUS_PAGES_SHORT = 32
+STATUS_NONFINITE = 64
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+F32, BF16 = 0, 1
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_TOO_SMALL, ERR_CUDA = 0, -1, -2, -3, -4
 
@@ -53,6 +61,34 @@ class Cfg:
                     self.sm_scale, self.d_rope)
 
 
+class CRopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("orig_len", ctypes.c_int32),
+                ("factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double)]
+
+
+@dataclass(frozen=True)
+class RopeScaling:
+    """Frequencies of a stretched context (``lla_rope_scaling``)."""
+    kind: str = "none"       # "none", "linear", "ntk" or "yarn"
+    factor: float = 1.0
+    orig_len: int = 1        # yarn: trained context
+    beta_fast: float = 0.0   # yarn; 0 selects 32
+    beta_slow: float = 0.0   # yarn; 0 selects 1
+
+    def c(self) -> CRopeScaling:
+        if self.kind not in ROPE_SCALES:
+            raise ValueError(f"rope scaling kind {self.kind!r} not in {sorted(ROPE_SCALES)}")
+        return CRopeScaling(ROPE_SCALES[self.kind], self.orig_len, self.factor, self.beta_fast,
+                            self.beta_slow)
+
+
+class CQ8Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page", ctypes.c_int32)]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -c \"import __graft_entry__ as g; "
                       "g.build()\"` (nvcc, sm_100a). There is no CPU fallback.")
@@ -61,6 +97,7 @@ lib = ctypes.CDLL(LIB_PATH)
 
 _P = ctypes.c_void_p
 _CFG = ctypes.POINTER(CCfg)
+_Q8 = ctypes.POINTER(CQ8Cache)
 _I32, _I64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 SIGNATURES = {
@@ -88,6 +125,19 @@ SIGNATURES = {
     "lla_full_decode_launches": (ctypes.c_int, [_CFG, _I32, _I32]),
     "lla_full_decode_attn": (ctypes.c_int, [_CFG, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P,
                                             _P, _P, _P, _SZ, _P]),
+    "lla_rope_table_scaled": (ctypes.c_int, [_CFG, ctypes.POINTER(CRopeScaling), _I32, _P, _SZ, _P]),
+    "lla_rope_apply": (ctypes.c_int, [_CFG, _P, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _I64,
+                                      _P, _I64, _P, _P]),
+    "lla_page_map": (ctypes.c_int, [_I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _I64, _P, _P, _P,
+                                    _P, _P]),
+    "lla_q8_cache_bytes": (_SZ, [_CFG, _I32, _I32]),
+    "lla_q8_append": (ctypes.c_int, [_CFG, _Q8, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _P,
+                                     _P, _P, _I64, _P, _I64, _P, _P]),
+    "lla_q8_read": (ctypes.c_int, [_CFG, _Q8, _I64, _P, _P, _P, _P, _P]),
+    "lla_q8_decode_workspace_bytes": (_SZ, [_CFG, _I32, _I32]),
+    "lla_q8_decode_launches": (ctypes.c_int, [_CFG, _I32, _I32]),
+    "lla_q8_decode_attn": (ctypes.c_int, [_CFG, _Q8, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _P,
+                                          _P, _P, _P, _P, _P, _SZ, _P]),
 }
 for _name, (_res, _args) in SIGNATURES.items():
     _fn = getattr(lib, _name)

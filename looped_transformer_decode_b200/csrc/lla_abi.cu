@@ -70,6 +70,55 @@ bool mul_ok(int64_t a, int64_t b, int64_t* out) {
   return true;
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// log2 of a supported page size, or -1.
+int page_shift(int page) {
+  return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : -1;
+}
+
+int check_rows(const char* who, int layout, int dtype) {
+  if (layout != LLA_ROPE_HALF && layout != LLA_ROPE_INTERLEAVED)
+    return fail(LLA_ERR_INVALID, "%s: layout %d unknown", who, layout);
+  if (dtype != LLA_F32 && dtype != LLA_BF16)
+    return fail(LLA_ERR_UNSUPPORTED, "%s: dtype %d is neither LLA_F32 nor LLA_BF16", who, dtype);
+  return LLA_OK;
+}
+
+// Bytes that n rows of `row` elements at a stride cover; false for a bad stride.
+bool check_stride(int64_t stride, int64_t row, int size, int64_t n, int64_t* bytes) {
+  int64_t to_last, elements;
+  if (stride % (16 / size) || (n > 1 && stride < row) || stride < 0) return false;
+  if (!mul_ok(stride, n - 1, &to_last) || to_last > INT64_MAX / 8 - row) return false;
+  elements = to_last + row;
+  *bytes = elements * size;
+  return true;
+}
+
+int check_q8(const char* who, const lla_q8_cache* c) {
+  if (!c) return fail(LLA_ERR_INVALID, "%s: cache is NULL", who);
+  if (page_shift(c->page) < 0)
+    return fail(LLA_ERR_UNSUPPORTED, "%s: page=%d not in {16, 32, 64, 128}", who, c->page);
+  if (c->n_pages < 0 || (int64_t)c->n_pages * c->page > (int64_t)INT32_MAX * 64)
+    return fail(LLA_ERR_INVALID, "%s: n_pages=%d out of range", who, c->n_pages);
+  if (c->n_pages == 0) return LLA_OK;
+  const void* ptrs[] = {c->k, c->v, c->k_scale, c->v_scale};
+  for (const void* p : ptrs) {
+    if (!p) return fail(LLA_ERR_INVALID, "%s: NULL cache pointer", who);
+    if (!aligned16(p)) return fail(LLA_ERR_INVALID, "%s: cache pointer not 16-byte aligned", who);
+  }
+  return LLA_OK;
+}
+
+int check_batch(const char* who, int B, int max_pages, int page) {
+  if (B < 0 || max_pages < 0)
+    return fail(LLA_ERR_INVALID, "%s: B and max_pages must be >= 0", who);
+  if (B > 65535) return fail(LLA_ERR_UNSUPPORTED, "%s: B=%d above 65535", who, B);
+  if ((int64_t)max_pages * page > INT32_MAX)
+    return fail(LLA_ERR_UNSUPPORTED, "%s: max_pages * page must be below 2^31", who);
+  return LLA_OK;
+}
+
 int cuda_fail(cudaError_t e, const char* what) {
   return fail(LLA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -196,7 +245,7 @@ extern "C" {
 
 const char* lla_last_error(void) { return g_err.c_str(); }
 
-const char* lla_version(void) { return "lla-b200 0.2 (sm_100a)"; }
+const char* lla_version(void) { return "lla-b200 0.3 (sm_100a)"; }
 
 int lla_ratio(const lla_cfg* cfg, int64_t* num, int64_t* den) {
   int e = check_cfg(cfg);
@@ -562,6 +611,315 @@ int lla_full_decode_attn(const lla_cfg* cfg, const void* rope_table, int32_t rop
   const void* vb = n_cap > 0 ? static_cast<const void*>(v_full) : ws;
   cudaError_t ce = launch_full_decode(p, kb, vb, pl.grid, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return cuda_fail(ce, "lla_full_decode_attn launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------- rotary positions
+
+int lla_rope_table_scaled(const lla_cfg* cfg, const lla_rope_scaling* sc, int32_t max_pos,
+                          void* table, size_t table_bytes, void* stream) {
+  int e = check_cfg(cfg);
+  if (e) return e;
+  if (!sc) return fail(LLA_ERR_INVALID, "lla_rope_table_scaled: scaling is NULL");
+  if (sc->kind < LLA_ROPE_SCALE_NONE || sc->kind > LLA_ROPE_SCALE_YARN)
+    return fail(LLA_ERR_INVALID, "rope scaling kind %d unknown", sc->kind);
+  if (sc->kind != LLA_ROPE_SCALE_NONE && (!(sc->factor >= 1.0) || !std::isfinite(sc->factor)))
+    return fail(LLA_ERR_INVALID, "rope scaling factor=%g must be finite and >= 1", sc->factor);
+  if (sc->kind == LLA_ROPE_SCALE_YARN) {
+    if (sc->orig_len < 1) return fail(LLA_ERR_INVALID, "orig_len=%d must be >= 1", sc->orig_len);
+    const double fast = sc->beta_fast == 0.0 ? 32.0 : sc->beta_fast;
+    const double slow = sc->beta_slow == 0.0 ? 1.0 : sc->beta_slow;
+    if (!(slow > 0.0) || !(fast > slow) || !std::isfinite(fast))
+      return fail(LLA_ERR_INVALID, "need 0 < beta_slow < beta_fast, got %g and %g", slow, fast);
+  }
+  if (max_pos < 1) return fail(LLA_ERR_INVALID, "max_pos=%d must be >= 1", max_pos);
+  if (!table || !aligned16(table)) return fail(LLA_ERR_INVALID, "table NULL or misaligned");
+  const size_t need = lla_rope_table_bytes(cfg, max_pos);
+  if (table_bytes < need)
+    return fail(LLA_ERR_TOO_SMALL, "rope table has %zu bytes, needs %zu", table_bytes, need);
+  cudaError_t ce = launch_rope_table_scaled(*cfg, *sc, max_pos, static_cast<float2*>(table),
+                                            static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return cuda_fail(ce, "lla_rope_table_scaled launch");
+  return ok();
+}
+
+int lla_rope_apply(const lla_cfg* cfg, const void* rope_table, int32_t rope_max_pos,
+                   int32_t layout, int32_t inverse, int32_t dtype, int64_t n_tok,
+                   int32_t n_heads, const int32_t* positions, const void* x, int64_t x_stride,
+                   void* y, int64_t y_stride, int32_t* status, void* stream) {
+  int e = check_cfg(cfg);
+  if (e) return e;
+  e = check_rows("lla_rope_apply", layout, dtype);
+  if (e) return e;
+  if (n_tok < 0) return fail(LLA_ERR_INVALID, "n_tok must be >= 0");
+  if (n_heads < 1 || n_heads > 4096)
+    return fail(LLA_ERR_UNSUPPORTED, "n_heads=%d outside [1, 4096]", n_heads);
+  if (rope_max_pos < 1) return fail(LLA_ERR_INVALID, "rope_max_pos must be >= 1");
+  if (n_tok == 0) return ok();
+  const int64_t row = (int64_t)n_heads * cfg->d_head;
+  const int size = dtype == LLA_BF16 ? 2 : 4;
+  int64_t chunks;
+  if (!mul_ok(n_tok, row / 8, &chunks) || chunks > (int64_t)INT32_MAX * 256)
+    return fail(LLA_ERR_UNSUPPORTED, "n_tok=%lld too large", (long long)n_tok);
+  if (!rope_table || !positions || !x || !y)
+    return fail(LLA_ERR_INVALID, "lla_rope_apply: NULL pointer argument");
+  if (!aligned16(rope_table) || !aligned16(x) || !aligned16(y) || !aligned4(positions))
+    return fail(LLA_ERR_INVALID, "lla_rope_apply: misaligned pointer");
+  if (status && !aligned4(status))
+    return fail(LLA_ERR_INVALID, "lla_rope_apply: status not 4-byte aligned");
+  int64_t xb, yb;
+  if (!check_stride(x_stride, row, size, n_tok, &xb) || !check_stride(y_stride, row, size, n_tok, &yb))
+    return fail(LLA_ERR_INVALID,
+                "lla_rope_apply: strides %lld, %lld must be multiples of 16 bytes and >= %lld",
+                (long long)x_stride, (long long)y_stride, (long long)row);
+  // x and y: the same rows, disjoint ranges, or rows that alternate at one stride
+  const uint64_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y);
+  const bool apart = xa + xb <= ya || ya + yb <= xa;
+  if (!apart && !(xa == ya && (x_stride == y_stride || n_tok == 1))) {
+    const uint64_t st = (uint64_t)x_stride * size, rb = (uint64_t)row * size;
+    const uint64_t by = (xa > ya ? xa - ya : ya - xa) % st;
+    if (x_stride != y_stride || by < rb || st - by < rb)
+      return fail(LLA_ERR_INVALID, "lla_rope_apply: rows of x and y overlap");
+  }
+  RopeApplyArgs a{};
+  a.rope = static_cast<const float2*>(rope_table);
+  a.rope_max_pos = rope_max_pos;
+  a.d = cfg->d_head;
+  a.rd = rotary_dims(*cfg);
+  a.layout = layout;
+  a.n_heads = n_heads;
+  a.bf16 = dtype == LLA_BF16;
+  a.sign = inverse ? -1.f : 1.f;
+  a.n_tok = n_tok;
+  a.x_stride = x_stride;
+  a.y_stride = y_stride;
+  a.positions = positions;
+  a.x = x;
+  a.y = y;
+  a.status = status;
+  cudaError_t ce = launch_rope_apply(a, static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return cuda_fail(ce, "lla_rope_apply launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------- pages
+
+int lla_page_map(int32_t B, int32_t page, int32_t max_pages, int32_t n_pages, int32_t* ctx_len,
+                 const int32_t* n_new, int32_t* block_table, int32_t* free_list, int32_t* n_free,
+                 int64_t tok_cap, int32_t* tok_start, int64_t* slot, int32_t* positions,
+                 int32_t* status, void* stream) {
+  if (B < 0 || max_pages < 0 || n_pages < 0 || tok_cap < 0)
+    return fail(LLA_ERR_INVALID, "lla_page_map: B, max_pages, n_pages and tok_cap must be >= 0");
+  const int shift = page_shift(page);
+  if (shift < 0) return fail(LLA_ERR_UNSUPPORTED, "page=%d not in {16, 32, 64, 128}", page);
+  if (B > 65535) return fail(LLA_ERR_UNSUPPORTED, "B=%d above 65535", B);
+  if ((int64_t)max_pages * page > INT32_MAX || tok_cap > INT32_MAX)
+    return fail(LLA_ERR_UNSUPPORTED, "max_pages * page and tok_cap must be below 2^31");
+  if (!n_free || !tok_start || (B && (!ctx_len || !n_new)) || (B && max_pages && !block_table) ||
+      (n_pages && !free_list) || (tok_cap && (!slot || !positions)))
+    return fail(LLA_ERR_INVALID, "lla_page_map: NULL pointer argument");
+  const void* words[] = {ctx_len, n_new, block_table, free_list, n_free, tok_start, positions, status};
+  for (const void* p : words)
+    if (!aligned4(p)) return fail(LLA_ERR_INVALID, "lla_page_map: misaligned pointer");
+  if (reinterpret_cast<uintptr_t>(slot) & 7u)
+    return fail(LLA_ERR_INVALID, "lla_page_map: slot not 8-byte aligned");
+  PageMapArgs a{};
+  a.B = B;
+  a.shift = shift;
+  a.max_pages = max_pages;
+  a.n_pages = n_pages;
+  a.tok_cap = tok_cap;
+  a.ctx_len = ctx_len;
+  a.n_new = n_new;
+  a.block_table = block_table;
+  a.free_list = free_list;
+  a.n_free = n_free;
+  a.tok_start = tok_start;
+  a.slot = slot;
+  a.positions = positions;
+  a.status = status;
+  cudaError_t ce = launch_page_map(a, static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return cuda_fail(ce, "lla_page_map launch");
+  return ok();
+}
+
+// ---------------------------------------------------------------- paged 8-bit cache
+
+size_t lla_q8_cache_bytes(const lla_cfg* cfg, int32_t n_pages, int32_t page) {
+  if (check_cfg(cfg) || n_pages < 0 || page_shift(page) < 0) return 0;
+  ok();
+  return (size_t)n_pages * cfg->H * page * cfg->d_head;
+}
+
+int lla_q8_append(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
+                  int32_t rope_max_pos, int32_t layout, int32_t dtype, int32_t B,
+                  int32_t max_pages, const int32_t* ctx_len, const int32_t* block_table,
+                  int32_t n_tok, const int32_t* tok_start, const int32_t* positions,
+                  const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                  int32_t* status, void* stream) {
+  int e = check_cfg(cfg);
+  if (e) return e;
+  e = check_q8("lla_q8_append", cache);
+  if (e) return e;
+  e = check_rows("lla_q8_append", layout, dtype);
+  if (e) return e;
+  e = check_batch("lla_q8_append", B, max_pages, cache->page);
+  if (e) return e;
+  if (n_tok < 0) return fail(LLA_ERR_INVALID, "n_tok must be >= 0");
+  if (rope_table && rope_max_pos < 1) return fail(LLA_ERR_INVALID, "rope_max_pos must be >= 1");
+  if (B == 0 || n_tok == 0 || cache->n_pages == 0 || max_pages == 0) return ok();
+  if (!ctx_len || !block_table || !tok_start || !k || !v || (rope_table && !positions))
+    return fail(LLA_ERR_INVALID, "lla_q8_append: NULL pointer argument");
+  if (!aligned16(rope_table) || !aligned16(k) || !aligned16(v) || !aligned4(ctx_len) ||
+      !aligned4(block_table) || !aligned4(tok_start) || !aligned4(positions) || !aligned4(status))
+    return fail(LLA_ERR_INVALID, "lla_q8_append: misaligned pointer");
+  const int64_t row = (int64_t)cfg->H * cfg->d_head;
+  const int size = dtype == LLA_BF16 ? 2 : 4;
+  int64_t bytes;
+  if (!check_stride(k_stride, row, size, n_tok, &bytes) ||
+      !check_stride(v_stride, row, size, n_tok, &bytes))
+    return fail(LLA_ERR_INVALID,
+                "lla_q8_append: strides %lld, %lld must be multiples of 16 bytes and >= %lld",
+                (long long)k_stride, (long long)v_stride, (long long)row);
+  Q8AppendArgs a{};
+  a.rope = static_cast<const float2*>(rope_table);
+  a.rope_max_pos = rope_max_pos;
+  a.layout = layout;
+  a.d = cfg->d_head;
+  a.rd = rotary_dims(*cfg);
+  a.H = cfg->H;
+  a.bf16 = dtype == LLA_BF16;
+  a.B = B;
+  a.shift = page_shift(cache->page);
+  a.max_pages = max_pages;
+  a.n_pages = cache->n_pages;
+  a.n_tok = n_tok;
+  a.ctx_len = ctx_len;
+  a.block_table = block_table;
+  a.tok_start = tok_start;
+  a.positions = positions;
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.kc = cache->k;
+  a.vc = cache->v;
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.status = status;
+  cudaError_t ce = launch_q8_append(a, static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return cuda_fail(ce, "lla_q8_append launch");
+  return ok();
+}
+
+int lla_q8_read(const lla_cfg* cfg, const lla_q8_cache* cache, int64_t n_rows,
+                const int64_t* slot, uint16_t* k_out, uint16_t* v_out, int32_t* status,
+                void* stream) {
+  int e = check_cfg(cfg);
+  if (e) return e;
+  e = check_q8("lla_q8_read", cache);
+  if (e) return e;
+  if (n_rows < 0) return fail(LLA_ERR_INVALID, "n_rows must be >= 0");
+  if (n_rows == 0) return ok();
+  int64_t chunks;
+  if (!mul_ok(n_rows, (int64_t)cfg->H * cfg->d_head / 8, &chunks) ||
+      chunks > (int64_t)INT32_MAX * 256)
+    return fail(LLA_ERR_UNSUPPORTED, "n_rows=%lld too large", (long long)n_rows);
+  if (!slot || !k_out || !v_out) return fail(LLA_ERR_INVALID, "lla_q8_read: NULL pointer argument");
+  if ((reinterpret_cast<uintptr_t>(slot) & 7u) || !aligned16(k_out) || !aligned16(v_out) ||
+      !aligned4(status))
+    return fail(LLA_ERR_INVALID, "lla_q8_read: misaligned pointer");
+  Q8ReadArgs a{};
+  a.d = cfg->d_head;
+  a.H = cfg->H;
+  a.shift = page_shift(cache->page);
+  a.n_pages = cache->n_pages;
+  a.n_rows = n_rows;
+  a.slot = slot;
+  a.kc = cache->k;
+  a.vc = cache->v;
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.k_out = reinterpret_cast<__nv_bfloat16*>(k_out);
+  a.v_out = reinterpret_cast<__nv_bfloat16*>(v_out);
+  a.status = status;
+  cudaError_t ce = launch_q8_read(a, static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return cuda_fail(ce, "lla_q8_read launch");
+  return ok();
+}
+
+size_t lla_q8_decode_workspace_bytes(const lla_cfg* cfg, int32_t B, int32_t n_cap) {
+  if (check_cfg(cfg)) return 0;
+  if (B < 0 || B > 65535 || n_cap < 0) {
+    fail(LLA_ERR_INVALID, "need 0 <= B <= 65535 and n_cap >= 0");
+    return 0;
+  }
+  ok();
+  return q8_decode_ws_bytes(*cfg, B, n_cap);
+}
+
+int lla_q8_decode_launches(const lla_cfg* cfg, int32_t B, int32_t n_cap) {
+  if (check_cfg(cfg) || B < 0 || B > 65535 || n_cap < 0) return -1;
+  return B ? 1 : 0;
+}
+
+int lla_q8_decode_attn(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
+                       int32_t rope_max_pos, int32_t layout, int32_t dtype, int32_t B,
+                       int32_t max_pages, const int32_t* ctx_len, const int32_t* block_table,
+                       const void* q, const void* k_self, const void* v_self,
+                       const int32_t* q_pos, void* out, void* ws, size_t ws_bytes,
+                       void* stream) {
+  int e = check_cfg(cfg);
+  if (e) return e;
+  e = check_q8("lla_q8_decode_attn", cache);
+  if (e) return e;
+  e = check_rows("lla_q8_decode_attn", layout, dtype);
+  if (e) return e;
+  e = check_batch("lla_q8_decode_attn", B, max_pages, cache->page);
+  if (e) return e;
+  if (rope_table && rope_max_pos < 1) return fail(LLA_ERR_INVALID, "rope_max_pos must be >= 1");
+  if (B == 0) return ok();
+  if (!ctx_len || (max_pages && !block_table) || !q || !out || !ws || (rope_table && !q_pos))
+    return fail(LLA_ERR_INVALID, "lla_q8_decode_attn: NULL pointer argument");
+  if (!k_self != !v_self)
+    return fail(LLA_ERR_INVALID, "lla_q8_decode_attn: k_self and v_self go together");
+  if (!aligned16(rope_table) || !aligned16(q) || !aligned16(k_self) || !aligned16(v_self) ||
+      !aligned16(out) || !aligned16(ws) || !aligned4(ctx_len) || !aligned4(block_table) ||
+      !aligned4(q_pos))
+    return fail(LLA_ERR_INVALID, "lla_q8_decode_attn: misaligned pointer");
+  const size_t need = q8_decode_ws_bytes(*cfg, B, max_pages * cache->page);
+  if (ws_bytes < need)
+    return fail(LLA_ERR_TOO_SMALL, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  Q8DecodeArgs a{};
+  a.rope = static_cast<const float2*>(rope_table);
+  a.rope_max_pos = rope_max_pos;
+  a.layout = layout;
+  a.d = cfg->d_head;
+  a.rd = rotary_dims(*cfg);
+  a.H = cfg->H;
+  a.bf16 = dtype == LLA_BF16;
+  a.B = B;
+  a.shift = page_shift(cache->page);
+  a.max_pages = max_pages;
+  a.n_pages = cache->n_pages;
+  const float scale = cfg->sm_scale > 0.f ? cfg->sm_scale : 1.0f / std::sqrt((float)cfg->d_head);
+  a.kappa = (float)((double)scale * 1.4426950408889634);  // log2(e): base-2 scores
+  a.ctx_len = ctx_len;
+  a.block_table = block_table;
+  a.q_pos = q_pos;
+  a.q = q;
+  a.k_self = k_self;
+  a.v_self = v_self;
+  a.kc = cache->k;
+  a.vc = cache->v;
+  a.ks = cache->k_scale;
+  a.vs = cache->v_scale;
+  a.out = out;
+  a.status = static_cast<int32_t*>(ws);
+  a.counter = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + 16);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
+  cudaError_t ce = launch_q8_decode(a, static_cast<cudaStream_t>(stream));
+  if (ce != cudaSuccess) return cuda_fail(ce, "lla_q8_decode_attn launch");
   return ok();
 }
 

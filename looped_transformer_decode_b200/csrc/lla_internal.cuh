@@ -173,6 +173,93 @@ cudaError_t launch_full_rebuild(const FullRebuildArgs& a, cudaStream_t s);
 cudaError_t launch_full_decode(const FullDecodeParams& p, const void* k_full, const void* v_full,
                                int grid, cudaStream_t s);
 
+// Rotary positions (lla_rope.cu).
+struct RopeApplyArgs {
+  const float2* rope;              // [rope_max_pos][rd/2]
+  int rope_max_pos, d, rd, layout, n_heads, bf16;
+  float sign;                      // 1, or -1 for the inverse rotation
+  long long n_tok, x_stride, y_stride;   // strides between tokens, in elements
+  const int32_t* positions;
+  const void* x;
+  void* y;
+  int32_t* status;
+};
+cudaError_t launch_rope_table_scaled(const lla_cfg& c, const lla_rope_scaling& sc, int max_pos,
+                                     float2* table, cudaStream_t s);
+cudaError_t launch_rope_apply(const RopeApplyArgs& a, cudaStream_t s);
+
+// Pages of a cache shared by sequences (lla_pages.cu).
+struct PageMapArgs {
+  int B, shift, max_pages, n_pages;   // 1 << shift tokens per page
+  bool fill_here;                     // the slots are written by the first kernel
+  long long tok_cap;
+  int32_t* ctx_len;
+  const int32_t* n_new;
+  int32_t* block_table;
+  int32_t* free_list;
+  int32_t* n_free;
+  int32_t* tok_start;
+  int64_t* slot;
+  int32_t* positions;
+  int32_t* status;
+};
+cudaError_t launch_page_map(PageMapArgs a, cudaStream_t s);
+
+// Paged 8-bit cache (lla_q8.cu).
+struct Q8AppendArgs {
+  const float2* rope;              // null: keys come rotated
+  int rope_max_pos, layout, d, rd, H, bf16;
+  int B, shift, max_pages, n_pages, n_tok;
+  const int32_t* ctx_len;          // lengths with the new tokens
+  const int32_t* block_table;
+  const int32_t* tok_start;
+  const int32_t* positions;
+  const void* k;
+  const void* v;
+  long long k_stride, v_stride;
+  int8_t* kc;
+  int8_t* vc;
+  float* ks;
+  float* vs;
+  int32_t* status;
+};
+struct Q8ReadArgs {
+  int d, H, shift, n_pages;
+  long long n_rows;
+  const int64_t* slot;
+  const int8_t* kc;
+  const int8_t* vc;
+  const float* ks;
+  const float* vs;
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  int32_t* status;
+};
+struct Q8DecodeArgs {
+  const float2* rope;              // null: q and k_self come rotated
+  int rope_max_pos, layout, d, rd, H, bf16;
+  int B, shift, max_pages, n_pages;
+  float kappa;                     // sm_scale * log2(e): scores are kept in base-2 units
+  const int32_t* ctx_len;
+  const int32_t* block_table;
+  const int32_t* q_pos;
+  const void* q;
+  const void* k_self;              // null: no in-flight token
+  const void* v_self;
+  const int8_t* kc;
+  const int8_t* vc;
+  const float* ks;
+  const float* vs;
+  void* out;
+  int32_t* status;                 // ws words [0], [1]
+  uint32_t* counter;               // ws word [4]: blocks finished in this call
+  float* partials;
+};
+cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s);
+cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
+size_t q8_decode_ws_bytes(const lla_cfg& c, int B, int n_cap);
+cudaError_t launch_q8_decode(const Q8DecodeArgs& a, cudaStream_t s);
+
 // Record `fmt` as the calling thread's lla_last_error() message; returns `code`.
 int set_error(int code, const char* fmt, ...);
 
