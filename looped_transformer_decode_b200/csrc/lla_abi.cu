@@ -917,7 +917,8 @@ int lla_q8_decode_attn(const lla_cfg* cfg, const lla_q8_cache* cache, const void
   a.out = out;
   a.status = static_cast<int32_t*>(ws);
   a.counter = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + 16);
-  a.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeader);
+  a.piece_counters = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + q8_decode_counters_at());
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + q8_decode_partials_at());
   cudaError_t ce = launch_q8_decode(a, static_cast<cudaStream_t>(stream));
   if (ce != cudaSuccess) return cuda_fail(ce, "lla_q8_decode_attn launch");
   return ok();

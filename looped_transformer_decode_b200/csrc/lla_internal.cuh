@@ -253,11 +253,14 @@ struct Q8DecodeArgs {
   void* out;
   int32_t* status;                 // ws words [0], [1]
   uint32_t* counter;               // ws word [4]: blocks finished in this call
-  float* partials;
+  uint32_t* piece_counters;        // [blocks]: pieces of the item that a block's range begins
+  float* partials;                 // [blocks][2][2 + d]
 };
 cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s);
 cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
 size_t q8_decode_ws_bytes(const lla_cfg& c, int B, int n_cap);
+size_t q8_decode_counters_at();
+size_t q8_decode_partials_at();
 cudaError_t launch_q8_decode(const Q8DecodeArgs& a, cudaStream_t s);
 
 // Record `fmt` as the calling thread's lla_last_error() message; returns `code`.

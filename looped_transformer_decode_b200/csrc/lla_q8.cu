@@ -15,6 +15,7 @@
 
 #include "lla_internal.cuh"
 #include "lla_rows.cuh"
+#include "lla_sm100.cuh"
 
 namespace lla {
 namespace {
@@ -188,125 +189,484 @@ __global__ void __launch_bounds__(256) q8_read_kernel(Q8ReadArgs a) {
 }
 
 // ---------------------------------------------------------------- decode attention
+//
+// q8_decode_kernel<T, D>: HBM-bound (2 D bytes per token and head against 4 D
+// operations), so the codes never become floats one by one:
+//   scores   q is split once per item into three 7-bit integers, q = qs (q1 2^14 + q2 2^7
+//            + q3), and the dot products of four codes are one instruction each, exact in
+//            int32 (dp4a); the page's scale multiplies the finished score.
+//   values   a token's weight times its page's value scale, relative to the largest so
+//            far, is a 24-bit integer; its three bytes, of four tokens each, meet the codes
+//            of four tokens and one dim in dp4a, exact in int32 until a new largest weight
+//            rescales the sum in fp32.
+// About 1.5 instructions per code instead of the five of convert-and-multiply.
+//
+// Work: the tokens of all (sequence, head) items, in tiles of 2 KB of keys, laid end to
+// end and cut into equal ranges, one per block, from the lengths on the device: uneven
+// sequences and few long ones load every SM alike.  Warps take a range's tiles in turn,
+// each with a ring of its own filled by bulk copies, so no warp waits for another
+// inside an item.  An item cut by a range's end leaves partials; the last block to bring
+// one merges them in order.
 
 constexpr int kQ8Warps = 4;
+constexpr int kQ8Threads = 32 * kQ8Warps;
+constexpr int kQ8BlocksPerSm = 3;
+constexpr int kQ8Stages = 4;
+constexpr int kQ8MinTiles = 4;              // tiles worth a block
+constexpr int kQ8FlushGroups = 8192;        // 4 * 255 * 128 per group and dim stays below 2^31
+constexpr float kQ8Weight = 16777215.f;     // 2^24 - 1
+
+template <int D>
+struct Q8Shape {
+  static constexpr int kGroups = D == 96 ? 1 : 128 / D;     // 16-token groups per tile
+  static constexpr int kTile = 16 * kGroups;                // tokens per tile
+  static constexpr int kWords = D / 32;                     // 4-code words per lane and row
+  static constexpr int kGroupBytes = 16 * D;
+  static constexpr int kHalf = kGroups * kGroupBytes;       // keys of a stage, then its values
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kRing = kQ8Stages * kStage;
+  // shared memory: rings, warp partials, rotated q, barriers, page ids
+  static constexpr int kPartOff = kQ8Warps * kRing;
+  static constexpr int kQOff = kPartOff + kQ8Warps * (D + 4) * 4;
+  static constexpr int kBarOff = kQOff + D * 4;
+  static constexpr int kIdOff = kBarOff + kQ8Warps * kQ8Stages * 8;
+  static constexpr int kBytes = kIdOff + kQ8Warps * kQ8Stages * 4 * 4;
+};
 
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// One block per (sequence, head): each warp takes every fourth token with its own
-// online softmax, lanes own dims lane, lane + 32, ...; the warps merge at the end.
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kQ8Warps) q8_decode_kernel(Q8DecodeArgs a) {
-  constexpr int N = D / 32;
-  __shared__ float qs[D];
-  __shared__ float part[kQ8Warps][D + 2];
-  const int h = blockIdx.x % a.H, b = blockIdx.x / a.H;
-  const long long bh = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* q = static_cast<const T*>(a.q) + bh * D;
-  int n = a.ctx_len[b];
-  const long long cap = (long long)a.max_pages << a.shift;
-  if (n < 0 || n > cap) {
-    if (threadIdx.x == 0) atomicOr(a.status, LLA_STATUS_CTX_RANGE);
-    n = n < 0 ? 0 : (int)cap;
-  }
-  if (threadIdx.x < D / 8) {
-    const bool turn = a.rope != nullptr;
-    const RowChunk rc = row_chunk(threadIdx.x, D, a.rd, turn ? a.layout : LLA_ROPE_INTERLEAVED);
-    float v[8];
-    load_chunk(q, rc, v);
-    if (turn) {
-      const int pos = checked_position(a.q_pos[b], a.rope_max_pos, a.status, threadIdx.x == 0);
-      rotate_chunk(a.rope + (size_t)pos * (a.rd / 2), rc, 1.f, v);
-    }
+// sum of four products, unsigned bytes of a with signed bytes of b
+__device__ __forceinline__ int dp4a_us(uint32_t a, uint32_t b, int c) {
+  int d;
+  asm("dp4a.u32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t* w) {
+  if constexpr (W == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x;
+    w[1] = u.y;
+    w[2] = u.z;
+    w[3] = u.w;
+  } else if constexpr (W == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x;
+    w[1] = u.y;
+  } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      qs[rc.lo + j] = v[j] * a.kappa;
-      qs[rc.hi + j] = v[4 + j] * a.kappa;
+    for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+}
+
+// Ring slot of tile t when the item's first tile is the warp's tile number `used`.
+__device__ __forceinline__ int used_slot(int t, int first, uint32_t used) {
+  return (used + (uint32_t)(t - first) / kQ8Warps) % kQ8Stages;
+}
+
+// Length of sequence b, clamped into its block table.
+__device__ __forceinline__ int q8_length(const Q8DecodeArgs& a, int b, bool tell) {
+  const long long cap = (long long)a.max_pages << a.shift;
+  const int n = a.ctx_len[b];
+  if (n >= 0 && n <= cap) return n;
+  if (tell) atomicOr(a.status, LLA_STATUS_CTX_RANGE);
+  return n < 0 ? 0 : (int)cap;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q8DecodeArgs a) {
+  using S = Q8Shape<D>;
+  constexpr int W = S::kWords;
+  extern __shared__ __align__(128) unsigned char sm[];
+  float* parts = reinterpret_cast<float*>(sm + S::kPartOff);      // [warps][4 + D]
+  float* qs = reinterpret_cast<float*>(sm + S::kQOff);
+  __shared__ long long scan[kQ8Threads];
+  __shared__ long long start_at;      // units before the sequence of the range's first one
+  __shared__ int start_b;
+  __shared__ int abort_word;
+  __shared__ int is_last;
+  volatile int* abort_flag = &abort_word;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  unsigned char* ring = sm + warp * S::kRing;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff) + warp * kQ8Stages;
+  int* ids = reinterpret_cast<int*>(sm + S::kIdOff) + warp * kQ8Stages * 4;
+
+  // ---------------------------------------------------------------- the block's range
+  // Units: one per tile and head, one for an empty item.
+  const int per = (a.B + kQ8Threads - 1) / kQ8Threads;
+  const int seg0 = min(tid * per, a.B), seg1 = min(seg0 + per, a.B);
+  long long mine = 0;
+  for (int b = seg0; b < seg1; ++b)
+    mine += max(1, (q8_length(a, b, blockIdx.x == 0) + S::kTile - 1) / S::kTile);
+  scan[tid] = mine;
+  if (tid == 0) {
+    abort_word = 0;
+    start_b = 0;
+    start_at = 0;
+  }
+  if (lane == 0) {
+    for (int s = 0; s < kQ8Stages; ++s) sm100::mbar_init(&bars[s], 1);
+    sm100::fence_mbar_init();
+  }
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll 8
+  for (int i = 0; i < kQ8Threads; ++i) {
+    const long long v = scan[i];
+    if (i < tid) before += v;
+    total += v;
+  }
+  const long long units = total * a.H;
+  const int G = (int)max(1LL, min((long long)gridDim.x, units / kQ8MinTiles));
+  const int c = blockIdx.x;
+  if (c >= G) return;
+  // range of block i: [cut(i), cut(i + 1))
+  auto cut = [&](int i) { return units * i / G; };
+  const long long u0 = cut(c), u1 = cut(c + 1);
+  {
+    long long at = before * a.H;
+    if (u0 >= at && u0 < at + mine * a.H) {
+      int b = seg0;
+      for (; b < seg1; ++b) {
+        const long long n =
+            (long long)max(1, (q8_length(a, b, false) + S::kTile - 1) / S::kTile) * a.H;
+        if (u0 < at + n) break;
+        at += n;
+      }
+      start_b = b;
+      start_at = at;
     }
   }
   __syncthreads();
-  float qr[N], o[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    qr[k] = qs[lane + 32 * k];
-    o[k] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-  for (int j = warp; j < n; j += kQ8Warps) {
-    const int page = a.block_table[(long long)b * a.max_pages + (j >> a.shift)];
-    if (page < 0 || page >= a.n_pages) {
-      bad = true;
+
+  // ---------------------------------------------------------------- its items
+  const int r = lane >> 3, col = lane & 7;          // token row of a group of four, dims' eighth
+  uint32_t used = 0;                                // tiles this warp has put through its ring
+  bool aborted = false;
+  int b = start_b;
+  long long seq_at = start_at;                      // first unit of sequence b
+  for (long long u = u0; u < u1;) {
+    const int n = q8_length(a, b, false);
+    const int tiles = max(1, (n + S::kTile - 1) / S::kTile);
+    if (u >= seq_at + (long long)tiles * a.H) {
+      seq_at += (long long)tiles * a.H;
+      ++b;
       continue;
     }
-    const long long ph = (long long)page * a.H + h;
-    const long long row = ((ph << a.shift) + (j & ((1 << a.shift) - 1))) * D;
-    float s = 0.f;
+    const int h = (int)((u - seq_at) / tiles);
+    const long long item0 = seq_at + (long long)h * tiles;
+    const int t0 = (int)(u - item0);
+    const int t1 = (int)min((long long)tiles, u1 - item0);
+    const size_t bh = (size_t)b * a.H + h;
+    const int32_t* table = a.block_table + (long long)b * a.max_pages;
+
+    // page id of this lane's group of tile t; -1 for tokens that are not there
+    auto group_id = [&](int t) {
+      const long long tok = (long long)t * S::kTile + lane * 16;
+      return lane < S::kGroups && t < t1 && tok < n ? table[tok >> a.shift] : -1;
+    };
+    bool bad = false;
+    auto issue = [&](int t, int id) {               // whole warp; tile t of this item
+      if (t >= t1) return;
+      const int s = used_slot(t, t0 + warp, used);
+      const long long tok = (long long)t * S::kTile + lane * 16;
+      const bool there = lane < S::kGroups && tok < n;
+      const bool ok = there && id >= 0 && id < a.n_pages;
+      bad |= there && !ok;
+      const unsigned live = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) sm100::mbar_arrive_expect_tx(&bars[s], __popc(live) * 2 * S::kGroupBytes);
+      if (lane < S::kGroups) ids[s * 4 + lane] = ok ? id : -1;
+      __syncwarp();
+      if (ok) {
+        const long long run = (((long long)id * a.H + h) << a.shift) + (tok & ((1 << a.shift) - 1));
+        unsigned char* st = ring + s * S::kStage + lane * S::kGroupBytes;
+        sm100::bulk_load(st, a.kc + run * D, S::kGroupBytes, &bars[s]);
+        sm100::bulk_load(st + S::kHalf, a.vc + run * D, S::kGroupBytes, &bars[s]);
+      }
+    };
+    const int first = t0 + warp;
 #pragma unroll
-    for (int k = 0; k < N; ++k) s = fmaf(qr[k], (float)a.kc[row + lane + 32 * k], s);
+    for (int k = 0; k < kQ8Stages; ++k)
+      if (!aborted) issue(first + k * kQ8Warps, group_id(first + k * kQ8Warps));
+    int next_id = group_id(first + kQ8Stages * kQ8Warps);
+
+    // q rotated at q_pos, into shared memory
+    const T* q = static_cast<const T*>(a.q) + bh * D;
+    if (tid < D / 8) {
+      const bool turn = a.rope != nullptr;
+      const RowChunk rc = row_chunk(tid, D, a.rd, turn ? a.layout : LLA_ROPE_INTERLEAVED);
+      float v[8];
+      load_chunk(q, rc, v);
+      if (turn) {
+        const int pos = checked_position(a.q_pos[b], a.rope_max_pos, a.status, tid == 0);
+        rotate_chunk(a.rope + (size_t)pos * (a.rd / 2), rc, 1.f, v);
+      }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= a.ks[ph];
-    if (s > m) {
-      const float f = exp2f(m - s);
-      l *= f;
-#pragma unroll
-      for (int k = 0; k < N; ++k) o[k] *= f;
-      m = s;
+      for (int j = 0; j < 4; ++j) {
+        qs[rc.lo + j] = v[j];
+        qs[rc.hi + j] = v[4 + j];
+      }
     }
-    const float p = exp2f(s - m), w = p * a.vs[ph];
-    l += p;
+    __syncthreads();
+    // this lane's dims as three signed digits of 7 bits, the largest |q| at 127 * 2^14
+    uint32_t q1[W], q2[W], q3[W];
+    float score_scale;
+    bool strange = false;                                       // a NaN or an infinity in q
+    {
+      float v[4 * W], amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < N; ++k) o[k] = fmaf(w, (float)a.vc[row + lane + 32 * k], o[k]);
-  }
-  if (bad && lane == 0) atomicOr(a.status, LLA_STATUS_PAGE_RANGE);
-  if (lane == 0) {
-    part[warp][0] = m;
-    part[warp][1] = l;
-  }
+      for (int j = 0; j < 4 * W; ++j) {
+        v[j] = qs[col * 4 * W + j];
+        amax = fmaxf(amax, fabsf(v[j]));
+        strange |= !(fabsf(v[j]) <= FLT_MAX);
+      }
+      strange = __any_sync(0xffffffffu, strange);
 #pragma unroll
-  for (int k = 0; k < N; ++k) part[warp][2 + lane + 32 * k] = o[k];
-  __syncthreads();
-  // merge with the in-flight token, whose score needs no rotation: both sit at q_pos
-  if (warp == 0) {
-    float self = -INFINITY;
-    if (a.k_self) {
-      const T* ksf = static_cast<const T*>(a.k_self) + bh * D;
-      float acc = 0.f;
+      for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      constexpr float kTop = 127.f * 16384.f;
+      const float inv = amax > kQ8Tiny ? kTop / amax : 0.f;
+      score_scale = strange ? 0.f : a.kappa * amax / kTop;      // strange: pl becomes NaN below
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        acc = fmaf(as_float(q[lane + 32 * k]), as_float(ksf[lane + 32 * k]), acc);
+      for (int w = 0; w < W; ++w) {
+        q1[w] = q2[w] = q3[w] = 0;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-      self = acc * a.kappa;
+        for (int j = 0; j < 4; ++j) {
+          int x = __float2int_rn(v[4 * w + j] * inv);
+          const int lo = ((x + 64) & 127) - 64;
+          x = (x - lo) >> 7;
+          const int mid = ((x + 64) & 127) - 64;
+          x = (x - mid) >> 7;
+          q1[w] |= (uint32_t)(x & 255) << (8 * j);
+          q2[w] |= (uint32_t)(mid & 255) << (8 * j);
+          q3[w] |= (uint32_t)(lo & 255) << (8 * j);
+        }
+      }
     }
-    float M = self;
-    for (int w = 0; w < kQ8Warps; ++w) M = fmaxf(M, part[w][0]);
-    const float fs = self > -INFINITY ? exp2f(self - M) : 0.f;
-    float L = fs, acc[N];
+
+    float m = -INFINITY, l = 0.f;     // largest score, sum of 2^(s - m)
+    float M = -INFINITY;              // largest score + log2(value scale): weight 2^24 - 1
+    float o[4 * W];
+    int acc1[4 * W], acc2[4 * W], acc3[4 * W];
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      acc[k] = fs > 0.f ? fs * as_float(static_cast<const T*>(a.v_self)[bh * D + lane + 32 * k]) : 0.f;
-    for (int w = 0; w < kQ8Warps; ++w) {
-      if (!(part[w][0] > -INFINITY)) continue;
-      const float f = exp2f(part[w][0] - M);
-      L = fmaf(part[w][1], f, L);
-#pragma unroll
-      for (int k = 0; k < N; ++k) acc[k] = fmaf(part[w][2 + lane + 32 * k], f, acc[k]);
+    for (int j = 0; j < 4 * W; ++j) {
+      o[j] = 0.f;
+      acc1[j] = acc2[j] = acc3[j] = 0;
     }
+    int groups = 0;
+    auto flush = [&](float f) {
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      put(static_cast<T*>(a.out) + bh * D + lane + 32 * k, L > 0.f ? acc[k] / L : 0.f);
+      for (int j = 0; j < 4 * W; ++j) {
+        o[j] = f * (o[j] + fmaf((float)acc1[j], 65536.f, fmaf((float)acc2[j], 256.f, (float)acc3[j])));
+        acc1[j] = acc2[j] = acc3[j] = 0;
+      }
+      groups = 0;
+    };
+
+    for (int t = first; t < t1 && !aborted; t += kQ8Warps) {
+      const int s = used_slot(t, first, used);
+      const uint32_t ph = ((used + (t - first) / kQ8Warps) / kQ8Stages) & 1u;
+      if (!sm100::mbar_wait(&bars[s], ph, abort_flag)) {
+        // copies already issued land before the block can end
+        for (int k = 0; k < kQ8Stages && t + k * kQ8Warps < t1; ++k) {
+          const uint32_t n_put = used + (t - first) / kQ8Warps + k;
+          const unsigned long long w0 = sm100::global_timer_ns();
+          while (!sm100::mbar_try_wait(&bars[n_put % kQ8Stages], (n_put / kQ8Stages) & 1u) &&
+                 sm100::global_timer_ns() - w0 < sm100::kWaitTimeoutNs) {
+          }
+        }
+        aborted = true;
+        break;
+      }
+      const unsigned char* st = ring + s * S::kStage;
+#pragma unroll
+      for (int g = 0; g < S::kGroups; ++g) {
+        const int id = ids[s * 4 + g];
+        if (id < 0) continue;                                   // warp-uniform
+        const float ksc = __ldg(a.ks + (long long)id * a.H + h) * score_scale;
+        const float vsc = __ldg(a.vs + (long long)id * a.H + h);
+        const unsigned char* kp = st + g * S::kGroupBytes + r * D + col * 4 * W;
+        float part[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t kw[W];
+          load_words<W>(kp + i * 4 * D, kw);
+          int s1 = 0, s2 = 0, s3 = 0;
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            s1 = __dp4a((int)kw[w], (int)q1[w], s1);
+            s2 = __dp4a((int)kw[w], (int)q2[w], s2);
+            s3 = __dp4a((int)kw[w], (int)q3[w], s3);
+          }
+          part[i] = fmaf((float)(s1 * 128 + s2), 128.f, (float)s3);
+        }
+        // sum over the row's eight lanes; lane keeps row r + 4 i, i from its column's bits
+        float x0 = (col & 4 ? part[2] : part[0]) +
+                   __shfl_xor_sync(0xffffffffu, col & 4 ? part[0] : part[2], 4);
+        float x1 = (col & 4 ? part[3] : part[1]) +
+                   __shfl_xor_sync(0xffffffffu, col & 4 ? part[1] : part[3], 4);
+        x0 = (col & 2 ? x1 : x0) + __shfl_xor_sync(0xffffffffu, col & 2 ? x0 : x1, 2);
+        x0 += __shfl_xor_sync(0xffffffffu, x0, 1);
+        const int i_own = (col >> 1) & 1 | (col >> 1) & 2;
+        const long long tok = (long long)t * S::kTile + g * 16 + r + 4 * i_own;
+        const float sc = tok < n ? x0 * ksc : -INFINITY;
+        float mt = sc;
+#pragma unroll
+        for (int off = 2; off < 32; off <<= 1)
+          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+        if (mt > m) {
+          l *= exp2f(m - mt);
+          m = mt;
+        }
+        const float lv = vsc > 0.f ? log2f(vsc) : -INFINITY;
+        if (mt + lv > M) {
+          flush(M > -INFINITY ? exp2f(M - (mt + lv)) : 0.f);
+          M = mt + lv;
+        } else if (groups >= kQ8FlushGroups) {
+          flush(1.f);
+        }
+        ++groups;
+        const float p = exp2f(sc - m);
+        l += col & 1 ? 0.f : p;
+        const uint32_t wt = lv > -INFINITY ? __float2uint_rn(exp2f(sc + lv - M) * kQ8Weight) : 0u;
+        // the four rows' weights, then their bytes: hi, mid, lo words of four tokens
+        const uint32_t w2 = __shfl_xor_sync(0xffffffffu, wt, 2);
+        const uint32_t e0 = col & 2 ? w2 : wt, e1 = col & 2 ? wt : w2;
+        const uint32_t f0 = __shfl_xor_sync(0xffffffffu, e0, 4);
+        const uint32_t f1 = __shfl_xor_sync(0xffffffffu, e1, 4);
+        const uint32_t g0 = col & 4 ? f0 : e0, g1 = col & 4 ? f1 : e1;
+        const uint32_t g2 = col & 4 ? e0 : f0, g3 = col & 4 ? e1 : f1;
+        const uint32_t a01 = __byte_perm(g0, g1, 0x5140), a23 = __byte_perm(g2, g3, 0x5140);
+        const uint32_t h01 = __byte_perm(g0, g1, 0x0062), h23 = __byte_perm(g2, g3, 0x0062);
+        const uint32_t wlo = __byte_perm(a01, a23, 0x5410), wmid = __byte_perm(a01, a23, 0x7632);
+        const uint32_t whi = __byte_perm(h01, h23, 0x5410);
+        uint32_t vw[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_words<W>(kp + S::kHalf + i * 4 * D, vw[i]);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          // four rows of four dims, turned into four dims of four rows
+          const uint32_t y0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
+          const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
+          const uint32_t y2 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+          const uint32_t y3 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+          const uint32_t dim[4] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632),
+                                   __byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc1[4 * w + j] = dp4a_us(whi, dim[j], acc1[4 * w + j]);
+            acc2[4 * w + j] = dp4a_us(wmid, dim[j], acc2[4 * w + j]);
+            acc3[4 * w + j] = dp4a_us(wlo, dim[j], acc3[4 * w + j]);
+          }
+        }
+      }
+      __syncwarp();                                             // the stage is read
+      issue(t + kQ8Stages * kQ8Warps, next_id);
+      next_id = group_id(t + (kQ8Stages + 1) * kQ8Warps);
+    }
+    if (t1 > first) used += (t1 - first + kQ8Warps - 1) / kQ8Warps;
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, LLA_STATUS_PAGE_RANGE);
+
+    // ---------------------------------------------------------------- merge the warps
+    flush(1.f);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    l += __shfl_xor_sync(0xffffffffu, l, 4);
+#pragma unroll
+    for (int off = 8; off < 32; off <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+      for (int j = 0; j < 4 * W; ++j) o[j] += __shfl_xor_sync(0xffffffffu, o[j], off);
+    }
+    float* pw = parts + warp * (D + 4);
+    if (r == 0) {
+      // sums of 2^(s - m) v
+      const float f = M > -INFINITY ? exp2f(M - m) * (1.f / kQ8Weight) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4 * W; ++j) pw[4 + col * 4 * W + j] = o[j] * f;
+      if (lane == 0) {
+        pw[0] = m;
+        pw[1] = l;
+      }
+    }
+    __syncthreads();
+    float pm = -INFINITY, pl = 0.f, po = 0.f;
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) pm = fmaxf(pm, parts[w * (D + 4)]);
+    if (pm > -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kQ8Warps; ++w) {
+        const float f = exp2f(parts[w * (D + 4)] - pm);
+        pl = fmaf(parts[w * (D + 4) + 1], f, pl);
+        if (tid < D) po = fmaf(parts[w * (D + 4) + 4 + tid], f, po);
+      }
+    }
+
+    // ---------------------------------------------------------------- the item's other blocks
+    auto block_of = [&](long long x) { return (int)(((x + 1) * G - 1) / units); };
+    bool finish = true;
+    const int c0 = block_of(item0), c1 = block_of(item0 + tiles - 1);
+    if (c1 > c0) {
+      // slot 0: the first item of a block's range, slot 1: a later one, which is its last
+      float* mine_p = a.partials + (size_t)(2 * c + (u == u0 ? 0 : 1)) * (D + 2);
+      if (tid < D) __stcg(mine_p + 2 + tid, po);
+      if (tid == 0) {
+        __stcg(mine_p, pm);
+        __stcg(mine_p + 1, pl);
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        const unsigned got = atomicAdd(a.piece_counters + c0, 1u);
+        is_last = got == (unsigned)(c1 - c0);
+        if (is_last) a.piece_counters[c0] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      finish = is_last;
+      if (finish) {
+        const float* first_p = a.partials + (size_t)(2 * c0 + (cut(c0) == item0 ? 0 : 1)) * (D + 2);
+        pm = -INFINITY;
+        for (int i = c0; i <= c1; ++i)
+          pm = fmaxf(pm, __ldcg(i == c0 ? first_p : a.partials + (size_t)2 * i * (D + 2)));
+        pl = po = 0.f;
+        if (pm > -INFINITY)
+          for (int i = c0; i <= c1; ++i) {
+            const float* pp = i == c0 ? first_p : a.partials + (size_t)2 * i * (D + 2);
+            const float f = exp2f(__ldcg(pp) - pm);
+            pl = fmaf(__ldcg(pp + 1), f, pl);
+            if (tid < D) po = fmaf(__ldcg(pp + 2 + tid), f, po);
+          }
+      }
+    }
+    if (finish) {
+      // the in-flight token, whose score needs no rotation: both sit at q_pos
+      if (a.k_self) {
+        const T* ksf = static_cast<const T*>(a.k_self) + bh * D;
+        float dot = 0.f;
+        for (int j = lane; j < D; j += 32) dot = fmaf(as_float(q[j]), as_float(ksf[j]), dot);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        const float self = dot * a.kappa, top = fmaxf(pm, self);
+        const float f = pm > -INFINITY ? exp2f(pm - top) : 0.f, fs = exp2f(self - top);
+        pl = fmaf(pl, f, fs);
+        if (tid < D)
+          po = fmaf(po, f, fs * as_float(static_cast<const T*>(a.v_self)[bh * D + tid]));
+      }
+      if (strange && pl != 0.f) pl = NAN;
+      if (tid < D) put(static_cast<T*>(a.out) + bh * D + tid, pl == 0.f ? 0.f : po / pl);
+    }
+    __syncthreads();                                            // parts, qs and is_last are free
+    u = item0 + t1;
   }
+  if (aborted && lane == 0) atomicOr(a.status, LLA_STATUS_TIMEOUT);
   // the last block to finish publishes the call's status word and re-arms the counter
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     __threadfence();
-    if (atomicAdd(a.counter, 1u) == gridDim.x - 1) {
+    if (atomicAdd(a.counter, 1u) == (unsigned)G - 1) {
       __threadfence();
       a.status[1] = atomicExch(&a.status[0], 0);
       atomicExch(a.counter, 0u);
@@ -314,17 +674,33 @@ __global__ void __launch_bounds__(32 * kQ8Warps) q8_decode_kernel(Q8DecodeArgs a
   }
 }
 
+int q8_max_blocks() { return sm_count() * kQ8BlocksPerSm; }
+
+template <typename T, int D>
+cudaError_t launch_decode_td(const Q8DecodeArgs& a, cudaStream_t s) {
+  using S = Q8Shape<D>;
+  cudaError_t e = cudaFuncSetAttribute(q8_decode_kernel<T, D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (e != cudaSuccess) return e;
+  const long long tiles =
+      (((long long)a.max_pages << a.shift) + S::kTile - 1) / S::kTile;
+  const long long units = (long long)a.B * a.H * (tiles > 0 ? tiles : 1);
+  long long grid = units / kQ8MinTiles;
+  if (grid > q8_max_blocks()) grid = q8_max_blocks();
+  if (grid < 1) grid = 1;
+  q8_decode_kernel<T, D><<<(unsigned)grid, kQ8Threads, S::kBytes, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_decode_t(const Q8DecodeArgs& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)a.B * a.H;
   switch (a.d) {
-    case 32: q8_decode_kernel<T, 32><<<grid, 32 * kQ8Warps, 0, s>>>(a); break;
-    case 64: q8_decode_kernel<T, 64><<<grid, 32 * kQ8Warps, 0, s>>>(a); break;
-    case 96: q8_decode_kernel<T, 96><<<grid, 32 * kQ8Warps, 0, s>>>(a); break;
-    case 128: q8_decode_kernel<T, 128><<<grid, 32 * kQ8Warps, 0, s>>>(a); break;
+    case 32: return launch_decode_td<T, 32>(a, s);
+    case 64: return launch_decode_td<T, 64>(a, s);
+    case 96: return launch_decode_td<T, 96>(a, s);
+    case 128: return launch_decode_td<T, 128>(a, s);
     default: return cudaErrorNotSupported;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace
@@ -344,7 +720,12 @@ cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-size_t q8_decode_ws_bytes(const lla_cfg& c, int B, int n_cap) { return kWsHeader; }
+// Workspace: header, one counter per block, two partials per block.
+size_t q8_decode_counters_at() { return kWsHeader; }
+size_t q8_decode_partials_at() { return kWsHeader + align_up((size_t)q8_max_blocks() * 4, 256); }
+size_t q8_decode_ws_bytes(const lla_cfg& c, int, int) {
+  return q8_decode_partials_at() + (size_t)q8_max_blocks() * 2 * (c.d_head + 2) * 4;
+}
 
 cudaError_t launch_q8_decode(const Q8DecodeArgs& a, cudaStream_t s) {
   return a.bf16 ? launch_decode_t<__nv_bfloat16>(a, s) : launch_decode_t<float>(a, s);

@@ -435,6 +435,32 @@ def test_decode_of_zero_scales_and_extreme_codes():
 
 
 @pytest.mark.gpu
+def test_decode_of_queries_that_are_not_numbers():
+    """A NaN or an infinity in q or k_self reaches its own head only; an empty row stays zero.
+    A score of minus infinity (q negative where k_self is infinite) has weight zero."""
+    cfg, page = cfg_of(3, 64), 16
+    cache = random_cache(np.random.default_rng(2), cfg, 4, page)
+    q = torch.randn((2, 3, 64), device="cuda")
+    k = torch.randn((2, 3, 64), device="cuda")
+    args = (i32([20, 0]), i32([[0, 1], [2, 3]]))
+    want = lla.q8_decode_attn(cfg, None, cache, *args, q, k, k, None)
+    alone = lla.q8_decode_attn(cfg, None, cache, *args, q, None, None, None)
+    for bad in (float("nan"), float("inf")):
+        for which in (0, 1):
+            rows = [q.clone(), k.clone()]
+            rows[which][:, 1, 5] = bad
+            got = lla.q8_decode_attn(cfg, None, cache, *args, rows[0], rows[1], k, None)
+            assert got[1, 1].isnan().all()
+            if which == 1 and bad == float("inf") and q[0, 1, 5] < 0:
+                assert torch.allclose(got[0, 1], alone[0, 1], rtol=1e-6)
+            else:
+                assert got[0, 1].isnan().all()
+            assert torch.equal(got[:, 0::2], want[:, 0::2])
+            got = lla.q8_decode_attn(cfg, None, cache, *args, rows[0], None, None, None)
+            assert not got[1].any() and got[0, 1].isnan().all() == (which == 0)
+
+
+@pytest.mark.gpu
 def test_decode_of_damaged_lists():
     cfg, page = cfg_of(2, 64), 16
     g = np.random.default_rng(11)
