@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(256) q8_read_kernel(Q8ReadArgs a) {
 //            rescales the sum in fp32.
 // About 1.5 instructions per code instead of the five of convert-and-multiply.
 //
-// Work: the tokens of all (sequence, head) items, in tiles of 2 KB of keys, laid end to
+// Work: the tokens of all (sequence, head) items, in tiles of 4 KB of keys, laid end to
 // end and cut into equal ranges, one per block, from the lengths on the device: uneven
 // sequences and few long ones load every SM alike.  Warps take a range's tiles in turn,
 // each with a ring of its own filled by bulk copies, so no warp waits for another
@@ -211,26 +211,26 @@ __global__ void __launch_bounds__(256) q8_read_kernel(Q8ReadArgs a) {
 constexpr int kQ8Warps = 4;
 constexpr int kQ8Threads = 32 * kQ8Warps;
 constexpr int kQ8BlocksPerSm = 3;
-constexpr int kQ8Stages = 4;
+constexpr int kQ8Stages = 2;
 constexpr int kQ8MinTiles = 4;              // tiles worth a block
 constexpr int kQ8FlushGroups = 8192;        // 4 * 255 * 128 per group and dim stays below 2^31
 constexpr float kQ8Weight = 16777215.f;     // 2^24 - 1
+constexpr float kQ8SmallRef = 1e-31f;       // least reference of the weights
 
 template <int D>
 struct Q8Shape {
-  static constexpr int kGroups = D == 96 ? 1 : 128 / D;     // 16-token groups per tile
+  static constexpr int kGroups = D == 96 ? 2 : 256 / D;     // 16-token groups per tile
   static constexpr int kTile = 16 * kGroups;                // tokens per tile
   static constexpr int kWords = D / 32;                     // 4-code words per lane and row
   static constexpr int kGroupBytes = 16 * D;
   static constexpr int kHalf = kGroups * kGroupBytes;       // keys of a stage, then its values
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kRing = kQ8Stages * kStage;
-  // shared memory: rings, warp partials, rotated q, barriers, page ids
+  // shared memory: rings, warp partials, rotated q, barriers
   static constexpr int kPartOff = kQ8Warps * kRing;
   static constexpr int kQOff = kPartOff + kQ8Warps * (D + 4) * 4;
   static constexpr int kBarOff = kQOff + D * 4;
-  static constexpr int kIdOff = kBarOff + kQ8Warps * kQ8Stages * 8;
-  static constexpr int kBytes = kIdOff + kQ8Warps * kQ8Stages * 4 * 4;
+  static constexpr int kBytes = kBarOff + kQ8Warps * kQ8Stages * 8;
 };
 
 __device__ __forceinline__ float as_float(float x) { return x; }
@@ -263,11 +263,6 @@ __device__ __forceinline__ void load_words(const unsigned char* p, uint32_t* w) 
   }
 }
 
-// Ring slot of tile t when the item's first tile is the warp's tile number `used`.
-__device__ __forceinline__ int used_slot(int t, int first, uint32_t used) {
-  return (used + (uint32_t)(t - first) / kQ8Warps) % kQ8Stages;
-}
-
 // Length of sequence b, clamped into its block table.
 __device__ __forceinline__ int q8_length(const Q8DecodeArgs& a, int b, bool tell) {
   const long long cap = (long long)a.max_pages << a.shift;
@@ -293,7 +288,6 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char* ring = sm + warp * S::kRing;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff) + warp * kQ8Stages;
-  int* ids = reinterpret_cast<int*>(sm + S::kIdOff) + warp * kQ8Stages * 4;
 
   // ---------------------------------------------------------------- the block's range
   // Units: one per tile and head, one for an empty item.
@@ -364,35 +358,50 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     const size_t bh = (size_t)b * a.H + h;
     const int32_t* table = a.block_table + (long long)b * a.max_pages;
 
-    // page id of this lane's group of tile t; -1 for tokens that are not there
-    auto group_id = [&](int t) {
-      const long long tok = (long long)t * S::kTile + lane * 16;
-      return lane < S::kGroups && t < t1 && tok < n ? table[tok >> a.shift] : -1;
-    };
+    // Lane g < kGroups looks after group g of each tile: its page id (loaded two tiles
+    // ahead of the tile's use), its copies, its scales (loaded one tile ahead).
+    const size_t page_step = (size_t)a.H << a.shift;             // rows per page, all heads
+    const int8_t* kh = a.kc + ((size_t)h << a.shift) * D;
+    const int8_t* vh = a.vc + ((size_t)h << a.shift) * D;
     bool bad = false;
-    auto issue = [&](int t, int id) {               // whole warp; tile t of this item
-      if (t >= t1) return;
-      const int s = used_slot(t, t0 + warp, used);
-      const long long tok = (long long)t * S::kTile + lane * 16;
-      const bool there = lane < S::kGroups && tok < n;
+    auto group_id = [&](int t) {
+      if (lane >= S::kGroups || t >= t1) return -1;
+      const int tok = t * S::kTile + lane * 16;
+      return tok < n ? __ldg(table + (tok >> a.shift)) : -1;
+    };
+    auto checked = [&](int t, int id) {                          // -1 for what is not there
+      const bool there = lane < S::kGroups && t < t1 && t * S::kTile + lane * 16 < n;
       const bool ok = there && id >= 0 && id < a.n_pages;
       bad |= there && !ok;
-      const unsigned live = __ballot_sync(0xffffffffu, ok);
+      return ok ? id : -1;
+    };
+    auto issue = [&](int t, int id, uint32_t seq) {              // tile t, the warp's seq-th
+      if (t >= t1) return;
+      const int s = seq % kQ8Stages;
+      const unsigned live = __ballot_sync(0xffffffffu, id >= 0);
       if (lane == 0) sm100::mbar_arrive_expect_tx(&bars[s], __popc(live) * 2 * S::kGroupBytes);
-      if (lane < S::kGroups) ids[s * 4 + lane] = ok ? id : -1;
       __syncwarp();
-      if (ok) {
-        const long long run = (((long long)id * a.H + h) << a.shift) + (tok & ((1 << a.shift) - 1));
+      if (id >= 0) {
+        const int tok = t * S::kTile + lane * 16;
+        const size_t run = (id * page_step + (tok & ((1 << a.shift) - 1))) * D;
         unsigned char* st = ring + s * S::kStage + lane * S::kGroupBytes;
-        sm100::bulk_load(st, a.kc + run * D, S::kGroupBytes, &bars[s]);
-        sm100::bulk_load(st + S::kHalf, a.vc + run * D, S::kGroupBytes, &bars[s]);
+        sm100::bulk_load(st, kh + run, S::kGroupBytes, &bars[s]);
+        sm100::bulk_load(st + S::kHalf, vh + run, S::kGroupBytes, &bars[s]);
       }
     };
     const int first = t0 + warp;
-#pragma unroll
-    for (int k = 0; k < kQ8Stages; ++k)
-      if (!aborted) issue(first + k * kQ8Warps, group_id(first + k * kQ8Warps));
-    int next_id = group_id(first + kQ8Stages * kQ8Warps);
+    int id0 = -1, id1 = -1;                                      // tiles t and t + kQ8Warps
+    if (!aborted) {
+      id0 = group_id(first);
+      id1 = group_id(first + kQ8Warps);
+      id0 = checked(first, id0);
+      id1 = checked(first + kQ8Warps, id1);
+      issue(first, id0, used);
+      issue(first + kQ8Warps, id1, used + 1);
+    }
+    int id2 = group_id(first + 2 * kQ8Warps);
+    float ks0 = id0 >= 0 ? __ldg(a.ks + (size_t)id0 * a.H + h) : 0.f;
+    float vs0 = id0 >= 0 ? __ldg(a.vs + (size_t)id0 * a.H + h) : 0.f;
 
     // q rotated at q_pos, into shared memory
     const T* q = static_cast<const T*>(a.q) + bh * D;
@@ -447,8 +456,11 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       }
     }
 
-    float m = -INFINITY, l = 0.f;     // largest score, sum of 2^(s - m)
-    float M = -INFINITY;              // largest score + log2(value scale): weight 2^24 - 1
+    // Sums are relative to 2^m, m the largest score so far: l of 2^(s - m), o of
+    // 2^(s - m) v.  acc holds weights w = 2^(s - m) vs / R * (2^24 - 1) times codes, R
+    // the reference that no weight since the last flush exceeds.  A larger weight flushes
+    // acc into o; a larger score rescales l, o and R.
+    float m = -INFINITY, l = 0.f, R = 0.f, wf = 0.f;             // wf = (2^24 - 1) / R
     float o[4 * W];
     int acc1[4 * W], acc2[4 * W], acc3[4 * W];
 #pragma unroll
@@ -457,38 +469,46 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       acc1[j] = acc2[j] = acc3[j] = 0;
     }
     int groups = 0;
-    auto flush = [&](float f) {
+    auto flush = [&]() {
+      const float f = R * (1.f / kQ8Weight);
 #pragma unroll
       for (int j = 0; j < 4 * W; ++j) {
-        o[j] = f * (o[j] + fmaf((float)acc1[j], 65536.f, fmaf((float)acc2[j], 256.f, (float)acc3[j])));
+        o[j] = fmaf(f, fmaf((float)acc1[j], 65536.f, fmaf((float)acc2[j], 256.f, (float)acc3[j])),
+                    o[j]);
         acc1[j] = acc2[j] = acc3[j] = 0;
       }
       groups = 0;
     };
 
-    for (int t = first; t < t1 && !aborted; t += kQ8Warps) {
-      const int s = used_slot(t, first, used);
-      const uint32_t ph = ((used + (t - first) / kQ8Warps) / kQ8Stages) & 1u;
-      if (!sm100::mbar_wait(&bars[s], ph, abort_flag)) {
+    const int i_own = ((col >> 1) & 1) | ((col >> 1) & 2);      // row group this lane ends up with
+    uint32_t seq = used;
+    for (int t = first; t < t1 && !aborted; t += kQ8Warps, ++seq) {
+      const int s = seq % kQ8Stages;
+      const unsigned live = __ballot_sync(0xffffffffu, id0 >= 0);
+      // scales of the next tile, page ids of the one after it
+      const float ks1 = id1 >= 0 ? __ldg(a.ks + (size_t)id1 * a.H + h) : 0.f;
+      const float vs1 = id1 >= 0 ? __ldg(a.vs + (size_t)id1 * a.H + h) : 0.f;
+      id2 = checked(t + 2 * kQ8Warps, id2);
+      const int id3 = group_id(t + 3 * kQ8Warps);
+      if (!sm100::mbar_wait(&bars[s], (seq / kQ8Stages) & 1u, abort_flag)) {
         // copies already issued land before the block can end
         for (int k = 0; k < kQ8Stages && t + k * kQ8Warps < t1; ++k) {
-          const uint32_t n_put = used + (t - first) / kQ8Warps + k;
           const unsigned long long w0 = sm100::global_timer_ns();
-          while (!sm100::mbar_try_wait(&bars[n_put % kQ8Stages], (n_put / kQ8Stages) & 1u) &&
+          while (!sm100::mbar_try_wait(&bars[(seq + k) % kQ8Stages], ((seq + k) / kQ8Stages) & 1u) &&
                  sm100::global_timer_ns() - w0 < sm100::kWaitTimeoutNs) {
           }
         }
         aborted = true;
         break;
       }
-      const unsigned char* st = ring + s * S::kStage;
+      const unsigned char* st = ring + s * S::kStage + r * D + col * 4 * W;
+      const int rows_left = n - t * S::kTile - r - 4 * i_own;   // of this lane's row of group 0
 #pragma unroll
       for (int g = 0; g < S::kGroups; ++g) {
-        const int id = ids[s * 4 + g];
-        if (id < 0) continue;                                   // warp-uniform
-        const float ksc = __ldg(a.ks + (long long)id * a.H + h) * score_scale;
-        const float vsc = __ldg(a.vs + (long long)id * a.H + h);
-        const unsigned char* kp = st + g * S::kGroupBytes + r * D + col * 4 * W;
+        if (!(live >> g & 1)) continue;                         // warp-uniform
+        const float ksc = __shfl_sync(0xffffffffu, ks0, g) * score_scale;
+        const float vsc = __shfl_sync(0xffffffffu, vs0, g);
+        const unsigned char* kp = st + g * S::kGroupBytes;
         float part[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -503,35 +523,40 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
           }
           part[i] = fmaf((float)(s1 * 128 + s2), 128.f, (float)s3);
         }
-        // sum over the row's eight lanes; lane keeps row r + 4 i, i from its column's bits
+        // sum over the row's eight lanes; a lane keeps row r + 4 i_own
         float x0 = (col & 4 ? part[2] : part[0]) +
                    __shfl_xor_sync(0xffffffffu, col & 4 ? part[0] : part[2], 4);
-        float x1 = (col & 4 ? part[3] : part[1]) +
-                   __shfl_xor_sync(0xffffffffu, col & 4 ? part[1] : part[3], 4);
+        const float x1 = (col & 4 ? part[3] : part[1]) +
+                         __shfl_xor_sync(0xffffffffu, col & 4 ? part[1] : part[3], 4);
         x0 = (col & 2 ? x1 : x0) + __shfl_xor_sync(0xffffffffu, col & 2 ? x0 : x1, 2);
         x0 += __shfl_xor_sync(0xffffffffu, x0, 1);
-        const int i_own = (col >> 1) & 1 | (col >> 1) & 2;
-        const long long tok = (long long)t * S::kTile + g * 16 + r + 4 * i_own;
-        const float sc = tok < n ? x0 * ksc : -INFINITY;
-        float mt = sc;
+        const float sc = rows_left > 16 * g ? x0 * ksc : -INFINITY;
+        if (__any_sync(0xffffffffu, sc > m)) {
+          float mt = sc;
 #pragma unroll
-        for (int off = 2; off < 32; off <<= 1)
-          mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-        if (mt > m) {
-          l *= exp2f(m - mt);
+          for (int off = 2; off < 32; off <<= 1)
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+          const float f = exp2f(m - mt);                        // 0 the first time
           m = mt;
+          l *= f;
+          R *= f;
+#pragma unroll
+          for (int j = 0; j < 4 * W; ++j) o[j] *= f;
+          if (R < kQ8SmallRef) {                                // 1 / R stays finite
+            flush();
+            R = kQ8SmallRef;
+          }
+          wf = kQ8Weight / R;
         }
-        const float lv = vsc > 0.f ? log2f(vsc) : -INFINITY;
-        if (mt + lv > M) {
-          flush(M > -INFINITY ? exp2f(M - (mt + lv)) : 0.f);
-          M = mt + lv;
-        } else if (groups >= kQ8FlushGroups) {
-          flush(1.f);
-        }
-        ++groups;
         const float p = exp2f(sc - m);
         l += col & 1 ? 0.f : p;
-        const uint32_t wt = lv > -INFINITY ? __float2uint_rn(exp2f(sc + lv - M) * kQ8Weight) : 0u;
+        if (vsc > R || groups >= kQ8FlushGroups) {              // p <= 1
+          flush();
+          R = fmaxf(R, vsc);
+          wf = kQ8Weight / R;
+        }
+        ++groups;
+        const uint32_t wt = __float2uint_rn(fminf(p * (vsc * wf), kQ8Weight));
         // the four rows' weights, then their bytes: hi, mid, lo words of four tokens
         const uint32_t w2 = __shfl_xor_sync(0xffffffffu, wt, 2);
         const uint32_t e0 = col & 2 ? w2 : wt, e1 = col & 2 ? wt : w2;
@@ -564,14 +589,18 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
         }
       }
       __syncwarp();                                             // the stage is read
-      issue(t + kQ8Stages * kQ8Warps, next_id);
-      next_id = group_id(t + (kQ8Stages + 1) * kQ8Warps);
+      issue(t + kQ8Stages * kQ8Warps, id2, seq + kQ8Stages);
+      id0 = id1;
+      id1 = id2;
+      id2 = id3;
+      ks0 = ks1;
+      vs0 = vs1;
     }
     if (t1 > first) used += (t1 - first + kQ8Warps - 1) / kQ8Warps;
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, LLA_STATUS_PAGE_RANGE);
 
     // ---------------------------------------------------------------- merge the warps
-    flush(1.f);
+    flush();
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     l += __shfl_xor_sync(0xffffffffu, l, 4);
 #pragma unroll
@@ -582,10 +611,8 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     }
     float* pw = parts + warp * (D + 4);
     if (r == 0) {
-      // sums of 2^(s - m) v
-      const float f = M > -INFINITY ? exp2f(M - m) * (1.f / kQ8Weight) : 0.f;
 #pragma unroll
-      for (int j = 0; j < 4 * W; ++j) pw[4 + col * 4 * W + j] = o[j] * f;
+      for (int j = 0; j < 4 * W; ++j) pw[4 + col * 4 * W + j] = o[j];
       if (lane == 0) {
         pw[0] = m;
         pw[1] = l;
