@@ -10,6 +10,7 @@
 // its old value and rounds the codes already there again: growing by a constant
 // factor bounds the sum of those roundings by a geometric series, whereas following
 // every small rise would let a code survive many rescalings unrounded and drift.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 
@@ -201,12 +202,12 @@ __global__ void __launch_bounds__(256) q8_read_kernel(Q8ReadArgs a) {
 //            rescales the sum in fp32.
 // About 1.5 instructions per code instead of the five of convert-and-multiply.
 //
-// Work: the tokens of all (sequence, head) items, in tiles of 4 KB of keys, laid end to
-// end and cut into equal ranges, one per block, from the lengths on the device: uneven
-// sequences and few long ones load every SM alike.  Warps take a range's tiles in turn,
-// each with a ring of its own filled by bulk copies, so no warp waits for another
-// inside an item.  An item cut by a range's end leaves partials; the last block to bring
-// one merges them in order.
+// Work: the tokens of all (sequence, head) items, in tiles of 4 KB of keys, divided among
+// the blocks from the lengths on the device, so that uneven sequences and few long ones
+// load every SM alike (see "the block's range").  Warps take a block's tiles in turn, each
+// with a ring of its own filled by bulk copies, so no warp waits for another inside an
+// item.  Pieces of one item leave partials; the last block to bring one merges them in
+// order.
 
 constexpr int kQ8Warps = 4;
 constexpr int kQ8Threads = 32 * kQ8Warps;
@@ -272,6 +273,49 @@ __device__ __forceinline__ int q8_length(const Q8DecodeArgs& a, int b, bool tell
   return n < 0 ? 0 : (int)cap;
 }
 
+// What a block works on: tiles [t0, t1) of an item (sequence b, head h of n tokens).
+struct Q8Item {
+  int b, h, n, t0, t1;
+  int c0, pieces;       // first block with a piece of the item, and how many there are
+  int slot, first_slot; // partial slot (of two per block) of this block's and of c0's piece
+};
+
+__device__ __forceinline__ long long q8_div(long long x, int q) {
+  return x >> 32 ? x / q : (long long)((uint32_t)x / (uint32_t)q);
+}
+
+// Sums over the block before this thread and in all, of four ints each (0 <= sums < 2^31).
+struct Int4Scan {
+  int before[4], total[4];
+};
+__device__ __forceinline__ Int4Scan block_scan4(const int* v, int (*sums)[4]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    x[j] = v[j];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x[j], o);
+      if (lane >= o) x[j] += y;
+    }
+    if (lane == 31) sums[warp][j] = x[j];
+  }
+  __syncthreads();
+  Int4Scan r;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r.before[j] = x[j] - v[j];
+    r.total[j] = 0;
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) {
+      if (w < warp) r.before[j] += sums[w][j];
+      r.total[j] += sums[w][j];
+    }
+  }
+  return r;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q8DecodeArgs a) {
   using S = Q8Shape<D>;
@@ -279,26 +323,32 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   extern __shared__ __align__(128) unsigned char sm[];
   float* parts = reinterpret_cast<float*>(sm + S::kPartOff);      // [warps][4 + D]
   float* qs = reinterpret_cast<float*>(sm + S::kQOff);
-  __shared__ long long scan[kQ8Threads];
-  __shared__ long long start_at;      // units before the sequence of the range's first one
+  __shared__ long long sums64[kQ8Warps];
+  __shared__ int sums4[kQ8Warps][4];
+  __shared__ long long start_at;      // units (aligned: pieces) before the first item's sequence
   __shared__ int start_b;
-  __shared__ int abort_word;
-  __shared__ int is_last;
+  __shared__ int abort_word, is_last, told;
+  __shared__ float self_score;
   volatile int* abort_flag = &abort_word;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
   unsigned char* ring = sm + warp * S::kRing;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff) + warp * kQ8Stages;
 
   // ---------------------------------------------------------------- the block's range
-  // Units: one per tile and head, one for an empty item.
+  // Units: one per tile and head, one for an empty item.  When the grid can give every
+  // item blocks of its own, each block gets one piece of one item (`aligned`: pieces of up
+  // to q tiles, for the least q of four that fits the grid); otherwise range c is
+  // units [c q, c q + q) and may hold the end of one item, whole ones and a beginning.
   const int per = (a.B + kQ8Threads - 1) / kQ8Threads;
   const int seg0 = min(tid * per, a.B), seg1 = min(seg0 + per, a.B);
+  auto tiles_of = [&](int b, bool tell) {
+    return max(1, (int)(((long long)q8_length(a, b, tell) + S::kTile - 1) / S::kTile));
+  };
   long long mine = 0;
-  for (int b = seg0; b < seg1; ++b)
-    mine += max(1, (q8_length(a, b, blockIdx.x == 0) + S::kTile - 1) / S::kTile);
-  scan[tid] = mine;
+  for (int b = seg0; b < seg1; ++b) mine += tiles_of(b, c == 0);
   if (tid == 0) {
     abort_word = 0;
+    told = 0;
     start_b = 0;
     start_at = 0;
   }
@@ -306,30 +356,56 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     for (int s = 0; s < kQ8Stages; ++s) sm100::mbar_init(&bars[s], 1);
     sm100::fence_mbar_init();
   }
+  long long upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) sums64[warp] = upto;
   __syncthreads();
-  long long before = 0, total = 0;
-#pragma unroll 8
-  for (int i = 0; i < kQ8Threads; ++i) {
-    const long long v = scan[i];
-    if (i < tid) before += v;
-    total += v;
+  long long before = upto - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kQ8Warps; ++w) {
+    if (w < warp) before += sums64[w];
+    total += sums64[w];
   }
   const long long units = total * a.H;
-  const int G = (int)max(1LL, min((long long)gridDim.x, units / kQ8MinTiles));
-  const int c = blockIdx.x;
-  if (c >= G) return;
-  // range of block i: [cut(i), cut(i + 1))
-  auto cut = [&](int i) { return units * i / G; };
-  const long long u0 = cut(c), u1 = cut(c + 1);
+  int q = max(kQ8MinTiles, (int)q8_div(units + gridDim.x - 1, gridDim.x));
+  bool aligned = false;
+  int blocks, start_pieces = 0, mine_pieces = 0;
+  if ((long long)a.B * a.H <= gridDim.x) {
+    int qj[4], v[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) qj[j] = q + (q * j + 3) / 4;
+    for (int b = seg0; b < seg1; ++b) {
+      const int tiles = tiles_of(b, false);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += min((tiles + qj[j] - 1) / qj[j], (int)gridDim.x + 1);
+    }
+    const Int4Scan sc = block_scan4(v, sums4);
+#pragma unroll
+    for (int j = 3; j >= 0; --j)
+      if ((long long)sc.total[j] * a.H <= gridDim.x) {
+        aligned = true;
+        q = qj[j];
+        blocks = sc.total[j] * a.H;
+        start_pieces = sc.before[j];
+        mine_pieces = v[j];
+      }
+  }
+  if (!aligned) blocks = (int)q8_div(units + q - 1, q);
+  if (c >= blocks) return;
   {
-    long long at = before * a.H;
-    if (u0 >= at && u0 < at + mine * a.H) {
+    const long long x = aligned ? c : (long long)c * q;
+    long long at = (aligned ? start_pieces : before) * a.H;
+    if (x >= at && x < at + (aligned ? mine_pieces : mine) * a.H) {
       int b = seg0;
       for (; b < seg1; ++b) {
-        const long long n =
-            (long long)max(1, (q8_length(a, b, false) + S::kTile - 1) / S::kTile) * a.H;
-        if (u0 < at + n) break;
-        at += n;
+        const int tiles = tiles_of(b, false);
+        const long long len = (long long)(aligned ? (tiles + q - 1) / q : tiles) * a.H;
+        if (x < at + len) break;
+        at += len;
       }
       start_b = b;
       start_at = at;
@@ -341,85 +417,134 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   const int r = lane >> 3, col = lane & 7;          // token row of a group of four, dims' eighth
   uint32_t used = 0;                                // tiles this warp has put through its ring
   bool aborted = false;
-  int b = start_b;
-  long long seq_at = start_at;                      // first unit of sequence b
-  for (long long u = u0; u < u1;) {
-    const int n = q8_length(a, b, false);
-    const int tiles = max(1, (n + S::kTile - 1) / S::kTile);
-    if (u >= seq_at + (long long)tiles * a.H) {
-      seq_at += (long long)tiles * a.H;
-      ++b;
-      continue;
+  long long seq_at = start_at, u = (long long)c * q;   // range: first unit of sequence b, next unit
+  const long long u1 = min(u + q, units);
+  Q8Item it;
+  it.b = start_b;
+  // the item that unit u lies in (range), or the block's piece (aligned)
+  auto find_item = [&]() {
+    if (aligned) {
+      it.n = q8_length(a, it.b, false);
+      const int tiles = tiles_of(it.b, false), pieces = (tiles + q - 1) / q;
+      const int k = c - (int)seq_at;
+      it.h = k / pieces;
+      const int part = k - it.h * pieces, base = tiles / pieces, rem = tiles - base * pieces;
+      it.t0 = part * base + min(part, rem);
+      it.t1 = it.t0 + base + (part < rem ? 1 : 0);
+      it.c0 = c - part;
+      it.pieces = pieces;
+      it.slot = it.first_slot = 0;
+      return;
     }
-    const int h = (int)((u - seq_at) / tiles);
-    const long long item0 = seq_at + (long long)h * tiles;
-    const int t0 = (int)(u - item0);
-    const int t1 = (int)min((long long)tiles, u1 - item0);
-    const size_t bh = (size_t)b * a.H + h;
-    const int32_t* table = a.block_table + (long long)b * a.max_pages;
+    int tiles;
+    for (;;) {
+      it.n = q8_length(a, it.b, false);
+      tiles = tiles_of(it.b, false);
+      if (u < seq_at + (long long)tiles * a.H) break;
+      seq_at += (long long)tiles * a.H;
+      ++it.b;
+    }
+    it.h = (int)q8_div(u - seq_at, tiles);
+    const long long item0 = seq_at + (long long)it.h * tiles;
+    it.t0 = (int)(u - item0);
+    it.t1 = (int)min((long long)tiles, u1 - item0);
+    it.c0 = (int)q8_div(item0, q);
+    it.pieces = (int)q8_div(item0 + tiles - 1, q) - it.c0 + 1;
+    // slot 0: the first item of a block's range, slot 1: a later one, which is its last
+    it.slot = u == (long long)c * q ? 0 : 1;
+    it.first_slot = (long long)it.c0 * q == item0 ? 0 : 1;
+    u = item0 + it.t1;
+  };
 
-    // Lane g < kGroups looks after group g of each tile: its page id (loaded two tiles
-    // ahead of the tile's use), its copies, its scales (loaded one tile ahead).
-    const size_t page_step = (size_t)a.H << a.shift;             // rows per page, all heads
-    const int8_t* kh = a.kc + ((size_t)h << a.shift) * D;
-    const int8_t* vh = a.vc + ((size_t)h << a.shift) * D;
-    bool bad = false;
-    auto group_id = [&](int t) {
-      if (lane >= S::kGroups || t >= t1) return -1;
+  // Lane g < kGroups looks after group g of each tile: its page id (loaded two tiles
+  // ahead of the tile's use), its copies, its scales (loaded one tile ahead).
+  const size_t page_step = (size_t)a.H << a.shift;             // rows per page, all heads
+  bool bad = false;
+  auto group_id = [&](int t) {
+    if (lane >= S::kGroups || t >= it.t1) return -1;
+    const int tok = t * S::kTile + lane * 16;                  // lengths stay below 2^31
+    return tok < it.n ? __ldg(a.block_table + (long long)it.b * a.max_pages + (tok >> a.shift)) : -1;
+  };
+  auto checked = [&](int t, int id) {                          // -1 for what is not there
+    const bool there = lane < S::kGroups && t < it.t1 && t * S::kTile + lane * 16 < it.n;
+    const bool ok = there && id >= 0 && id < a.n_pages;
+    bad |= there && !ok;
+    return ok ? id : -1;
+  };
+  auto issue = [&](int t, int id, uint32_t seq) {              // tile t, the warp's seq-th
+    if (t >= it.t1) return;
+    const int s = seq % kQ8Stages;
+    const unsigned live = __ballot_sync(0xffffffffu, id >= 0);
+    if (lane == 0) sm100::mbar_arrive_expect_tx(&bars[s], __popc(live) * 2 * S::kGroupBytes);
+    __syncwarp();
+    if (id >= 0) {
       const int tok = t * S::kTile + lane * 16;
-      return tok < n ? __ldg(table + (tok >> a.shift)) : -1;
-    };
-    auto checked = [&](int t, int id) {                          // -1 for what is not there
-      const bool there = lane < S::kGroups && t < t1 && t * S::kTile + lane * 16 < n;
-      const bool ok = there && id >= 0 && id < a.n_pages;
-      bad |= there && !ok;
-      return ok ? id : -1;
-    };
-    auto issue = [&](int t, int id, uint32_t seq) {              // tile t, the warp's seq-th
-      if (t >= t1) return;
-      const int s = seq % kQ8Stages;
-      const unsigned live = __ballot_sync(0xffffffffu, id >= 0);
-      if (lane == 0) sm100::mbar_arrive_expect_tx(&bars[s], __popc(live) * 2 * S::kGroupBytes);
-      __syncwarp();
-      if (id >= 0) {
-        const int tok = t * S::kTile + lane * 16;
-        const size_t run = (id * page_step + (tok & ((1 << a.shift) - 1))) * D;
-        unsigned char* st = ring + s * S::kStage + lane * S::kGroupBytes;
-        sm100::bulk_load(st, kh + run, S::kGroupBytes, &bars[s]);
-        sm100::bulk_load(st + S::kHalf, vh + run, S::kGroupBytes, &bars[s]);
-      }
-    };
-    const int first = t0 + warp;
-    int id0 = -1, id1 = -1;                                      // tiles t and t + kQ8Warps
+      const size_t run = (id * page_step + ((size_t)it.h << a.shift) +
+                          (tok & ((1 << a.shift) - 1))) * D;
+      unsigned char* st = ring + s * S::kStage + lane * S::kGroupBytes;
+      sm100::bulk_load(st, a.kc + run, S::kGroupBytes, &bars[s]);
+      sm100::bulk_load(st + S::kHalf, a.vc + run, S::kGroupBytes, &bars[s]);
+    }
+  };
+  auto scale_of = [&](const float* scales, int id) {
+    return id >= 0 ? __ldg(scales + (size_t)id * a.H + it.h) : 0.f;
+  };
+  int id0 = -1, id1 = -1, id2 = -1;                            // tiles t, t + 4, t + 8
+  float ks0 = 0.f, vs0 = 0.f;
+  auto start_item = [&]() {
+    const int first = it.t0 + warp;
+    id0 = group_id(first);
+    id1 = group_id(first + kQ8Warps);
+    id2 = group_id(first + 2 * kQ8Warps);
+    id0 = checked(first, id0);
+    id1 = checked(first + kQ8Warps, id1);
     if (!aborted) {
-      id0 = group_id(first);
-      id1 = group_id(first + kQ8Warps);
-      id0 = checked(first, id0);
-      id1 = checked(first + kQ8Warps, id1);
       issue(first, id0, used);
       issue(first + kQ8Warps, id1, used + 1);
     }
-    int id2 = group_id(first + 2 * kQ8Warps);
-    float ks0 = id0 >= 0 ? __ldg(a.ks + (size_t)id0 * a.H + h) : 0.f;
-    float vs0 = id0 >= 0 ? __ldg(a.vs + (size_t)id0 * a.H + h) : 0.f;
+    ks0 = scale_of(a.ks, id0);
+    vs0 = scale_of(a.vs, id0);
+  };
+  find_item();
+  start_item();
+  for (bool more = true; more;) {
+    const int first = it.t0 + warp;
+    const size_t bh = (size_t)it.b * a.H + it.h;
 
-    // q rotated at q_pos, into shared memory
-    const T* q = static_cast<const T*>(a.q) + bh * D;
-    if (tid < D / 8) {
-      const bool turn = a.rope != nullptr;
-      const RowChunk rc = row_chunk(tid, D, a.rd, turn ? a.layout : LLA_ROPE_INTERLEAVED);
-      float v[8];
-      load_chunk(q, rc, v);
-      if (turn) {
-        const int pos = checked_position(a.q_pos[b], a.rope_max_pos, a.status, tid == 0);
-        rotate_chunk(a.rope + (size_t)pos * (a.rd / 2), rc, 1.f, v);
+    // q rotated at q_pos, into shared memory; the in-flight token's score, which needs no
+    // rotation, both sitting at q_pos
+    float v_own = 0.f;
+    if (tid < 32) {
+      float acc = 0.f;
+      if (tid < D / 8) {
+        const bool turn = a.rope != nullptr;
+        const RowChunk rc = row_chunk(tid, D, a.rd, turn ? a.layout : LLA_ROPE_INTERLEAVED);
+        float v[8], k[8];
+        load_chunk(static_cast<const T*>(a.q) + bh * D, rc, v);
+        if (a.k_self) {
+          load_chunk(static_cast<const T*>(a.k_self) + bh * D, rc, k);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc = fmaf(v[j], k[j], acc);
+        }
+        if (turn) {
+          const int pos = checked_position(a.q_pos[it.b], a.rope_max_pos, nullptr, false);
+          if (tid == 0 && pos != a.q_pos[it.b]) {
+            atomicOr(a.status, LLA_STATUS_POSITION_RANGE);
+            told = 1;
+          }
+          rotate_chunk(a.rope + (size_t)pos * (a.rd / 2), rc, 1.f, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qs[rc.lo + j] = v[j];
+          qs[rc.hi + j] = v[4 + j];
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        qs[rc.lo + j] = v[j];
-        qs[rc.hi + j] = v[4 + j];
-      }
+      for (int off = 8; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+      if (tid == 0) self_score = acc * a.kappa;
     }
+    if (a.k_self && tid < D) v_own = as_float(static_cast<const T*>(a.v_self)[bh * D + tid]);
     __syncthreads();
     // this lane's dims as three signed digits of 7 bits, the largest |q| at 127 * 2^14
     uint32_t q1[W], q2[W], q3[W];
@@ -482,17 +607,16 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
 
     const int i_own = ((col >> 1) & 1) | ((col >> 1) & 2);      // row group this lane ends up with
     uint32_t seq = used;
-    for (int t = first; t < t1 && !aborted; t += kQ8Warps, ++seq) {
+    for (int t = first; t < it.t1 && !aborted; t += kQ8Warps, ++seq) {
       const int s = seq % kQ8Stages;
       const unsigned live = __ballot_sync(0xffffffffu, id0 >= 0);
       // scales of the next tile, page ids of the one after it
-      const float ks1 = id1 >= 0 ? __ldg(a.ks + (size_t)id1 * a.H + h) : 0.f;
-      const float vs1 = id1 >= 0 ? __ldg(a.vs + (size_t)id1 * a.H + h) : 0.f;
+      const float ks1 = scale_of(a.ks, id1), vs1 = scale_of(a.vs, id1);
       id2 = checked(t + 2 * kQ8Warps, id2);
       const int id3 = group_id(t + 3 * kQ8Warps);
       if (!sm100::mbar_wait(&bars[s], (seq / kQ8Stages) & 1u, abort_flag)) {
         // copies already issued land before the block can end
-        for (int k = 0; k < kQ8Stages && t + k * kQ8Warps < t1; ++k) {
+        for (int k = 0; k < kQ8Stages && t + k * kQ8Warps < it.t1; ++k) {
           const unsigned long long w0 = sm100::global_timer_ns();
           while (!sm100::mbar_try_wait(&bars[(seq + k) % kQ8Stages], ((seq + k) / kQ8Stages) & 1u) &&
                  sm100::global_timer_ns() - w0 < sm100::kWaitTimeoutNs) {
@@ -502,7 +626,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
         break;
       }
       const unsigned char* st = ring + s * S::kStage + r * D + col * 4 * W;
-      const int rows_left = n - t * S::kTile - r - 4 * i_own;   // of this lane's row of group 0
+      const int rows_left = it.n - t * S::kTile - r - 4 * i_own;   // of this lane's row of group 0
 #pragma unroll
       for (int g = 0; g < S::kGroups; ++g) {
         if (!(live >> g & 1)) continue;                         // warp-uniform
@@ -596,8 +720,19 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       ks0 = ks1;
       vs0 = vs1;
     }
-    if (t1 > first) used += (t1 - first + kQ8Warps - 1) / kQ8Warps;
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.status, LLA_STATUS_PAGE_RANGE);
+    if (it.t1 > first) used += (it.t1 - first + kQ8Warps - 1) / kQ8Warps;
+    if (__any_sync(0xffffffffu, bad) && lane == 0) {
+      atomicOr(a.status, LLA_STATUS_PAGE_RANGE);
+      told = 1;
+    }
+    bad = false;
+    // the next item's first tiles are on their way while this one is merged
+    const Q8Item now = it;
+    more = !aligned && u < u1;
+    if (more) {
+      find_item();
+      start_item();
+    }
 
     // ---------------------------------------------------------------- merge the warps
     flush();
@@ -632,68 +767,75 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     }
 
     // ---------------------------------------------------------------- the item's other blocks
-    auto block_of = [&](long long x) { return (int)(((x + 1) * G - 1) / units); };
     bool finish = true;
-    const int c0 = block_of(item0), c1 = block_of(item0 + tiles - 1);
-    if (c1 > c0) {
-      // slot 0: the first item of a block's range, slot 1: a later one, which is its last
-      float* mine_p = a.partials + (size_t)(2 * c + (u == u0 ? 0 : 1)) * (D + 2);
+    if (now.pieces > 1) {
+      float* mine_p = a.partials + (size_t)(2 * c + now.slot) * (D + 2);
       if (tid < D) __stcg(mine_p + 2 + tid, po);
       if (tid == 0) {
         __stcg(mine_p, pm);
         __stcg(mine_p + 1, pl);
       }
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
-        const unsigned got = atomicAdd(a.piece_counters + c0, 1u);
-        is_last = got == (unsigned)(c1 - c0);
-        if (is_last) a.piece_counters[c0] = 0;
+        __threadfence();
+        const unsigned got = atomicAdd(a.piece_counters + now.c0, 1u);
+        is_last = got == (unsigned)now.pieces - 1;
+        if (is_last) a.piece_counters[now.c0] = 0;
         __threadfence();
       }
       __syncthreads();
       finish = is_last;
       if (finish) {
-        const float* first_p = a.partials + (size_t)(2 * c0 + (cut(c0) == item0 ? 0 : 1)) * (D + 2);
+        // in the order of the pieces, four at a time
         pm = -INFINITY;
-        for (int i = c0; i <= c1; ++i)
-          pm = fmaxf(pm, __ldcg(i == c0 ? first_p : a.partials + (size_t)2 * i * (D + 2)));
         pl = po = 0.f;
-        if (pm > -INFINITY)
-          for (int i = c0; i <= c1; ++i) {
-            const float* pp = i == c0 ? first_p : a.partials + (size_t)2 * i * (D + 2);
-            const float f = exp2f(__ldcg(pp) - pm);
-            pl = fmaf(__ldcg(pp + 1), f, pl);
-            if (tid < D) po = fmaf(__ldcg(pp + 2 + tid), f, po);
+        for (int k0 = 0; k0 < now.pieces; k0 += 4) {
+          float mm[4], ll[4], oo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = k0 + k;
+            const float* pp = a.partials +
+                (size_t)(2 * (now.c0 + i) + (i == 0 ? now.first_slot : 0)) * (D + 2);
+            mm[k] = i < now.pieces ? __ldcg(pp) : -INFINITY;
+            ll[k] = i < now.pieces ? __ldcg(pp + 1) : 0.f;
+            oo[k] = i < now.pieces && tid < D ? __ldcg(pp + 2 + tid) : 0.f;
           }
+          const float top = fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])), pm);
+          if (!(top > -INFINITY)) continue;
+          const float f0 = exp2f(pm - top);
+          pl *= f0;
+          po *= f0;
+          pm = top;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float f = exp2f(mm[k] - top);
+            pl = fmaf(ll[k], f, pl);
+            po = fmaf(oo[k], f, po);
+          }
+        }
       }
     }
     if (finish) {
-      // the in-flight token, whose score needs no rotation: both sit at q_pos
       if (a.k_self) {
-        const T* ksf = static_cast<const T*>(a.k_self) + bh * D;
-        float dot = 0.f;
-        for (int j = lane; j < D; j += 32) dot = fmaf(as_float(q[j]), as_float(ksf[j]), dot);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        const float self = dot * a.kappa, top = fmaxf(pm, self);
+        const float self = self_score, top = fmaxf(pm, self);
         const float f = pm > -INFINITY ? exp2f(pm - top) : 0.f, fs = exp2f(self - top);
         pl = fmaf(pl, f, fs);
-        if (tid < D)
-          po = fmaf(po, f, fs * as_float(static_cast<const T*>(a.v_self)[bh * D + tid]));
+        po = fmaf(po, f, fs * v_own);
       }
       if (strange && pl != 0.f) pl = NAN;
       if (tid < D) put(static_cast<T*>(a.out) + bh * D + tid, pl == 0.f ? 0.f : po / pl);
     }
     __syncthreads();                                            // parts, qs and is_last are free
-    u = item0 + t1;
   }
-  if (aborted && lane == 0) atomicOr(a.status, LLA_STATUS_TIMEOUT);
+  if (aborted && lane == 0) {
+    atomicOr(a.status, LLA_STATUS_TIMEOUT);
+    told = 1;
+  }
   // the last block to finish publishes the call's status word and re-arms the counter
   __syncthreads();
   if (tid == 0) {
-    __threadfence();
-    if (atomicAdd(a.counter, 1u) == (unsigned)G - 1) {
+    if (told || c == 0) __threadfence();                        // block 0 tells of lengths
+    if (atomicAdd(a.counter, 1u) == (unsigned)blocks - 1) {
       __threadfence();
       a.status[1] = atomicExch(&a.status[0], 0);
       atomicExch(a.counter, 0u);
@@ -711,10 +853,9 @@ cudaError_t launch_decode_td(const Q8DecodeArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long tiles =
       (((long long)a.max_pages << a.shift) + S::kTile - 1) / S::kTile;
-  const long long units = (long long)a.B * a.H * (tiles > 0 ? tiles : 1);
-  long long grid = units / kQ8MinTiles;
-  if (grid > q8_max_blocks()) grid = q8_max_blocks();
-  if (grid < 1) grid = 1;
+  // at most one block per kQ8MinTiles tiles of every item
+  const long long per_item = std::max(1LL, (tiles + kQ8MinTiles - 1) / kQ8MinTiles);
+  const long long grid = std::min<long long>((long long)a.B * a.H * per_item, q8_max_blocks());
   q8_decode_kernel<T, D><<<(unsigned)grid, kQ8Threads, S::kBytes, s>>>(a);
   return cudaGetLastError();
 }
