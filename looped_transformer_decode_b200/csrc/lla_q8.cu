@@ -214,25 +214,42 @@ constexpr int kQ8Threads = 32 * kQ8Warps;
 constexpr int kQ8BlocksPerSm = 3;
 constexpr int kQ8Stages = 2;
 constexpr int kQ8MinTiles = 4;              // tiles worth a block
-constexpr int kQ8FlushGroups = 8192;        // 4 * 255 * 128 per group and dim stays below 2^31
-constexpr float kQ8Weight = 16777215.f;     // 2^24 - 1
+constexpr int kQ8ItemBlock = 12;            // start and merge of an item in tiles, for a block
+constexpr int kQ8ItemWarp = 4;              // and for a warp that has it to itself
+constexpr int kQ8FlushTiles = 4096;         // 2 * 4 * 255 * 128 per tile and dim stays below 2^31
+constexpr float kQ8Weight = 16777200.f;     // below 2^24 - 1 by more than a product's roundings
 constexpr float kQ8SmallRef = 1e-31f;       // least reference of the weights
 
 template <int D>
 struct Q8Shape {
-  static constexpr int kGroups = D == 96 ? 2 : 256 / D;     // 16-token groups per tile
-  static constexpr int kTile = 16 * kGroups;                // tokens per tile
-  static constexpr int kWords = D / 32;                     // 4-code words per lane and row
-  static constexpr int kGroupBytes = 16 * D;
-  static constexpr int kHalf = kGroups * kGroupBytes;       // keys of a stage, then its values
+  // A row's lanes hold 16 of its codes each (12 of 96); a warp's load covers kRows rows, and
+  // four of them are a group, the unit of the arithmetic.  kSubs 16-token blocks, each in
+  // one page, make a group; two groups make a tile.
+  static constexpr int kLanes = D == 96 ? 8 : D / 16;
+  static constexpr int kWords = D / kLanes / 4;             // 4-code words per lane and row
+  static constexpr int kRows = 32 / kLanes;
+  static constexpr int kGroup = 4 * kRows;
+  static constexpr int kSubs = kGroup / 16;
+  static constexpr int kScores = kGroup > 32 ? 2 : 1;       // scores per lane
+  static constexpr int kParts = 2 * kSubs;                  // 16-token blocks of a tile
+  static constexpr int kTile = 16 * kParts;                 // tokens per tile
+  static constexpr int kPartBytes = 16 * D;
+  static constexpr int kHalf = kParts * kPartBytes;         // keys of a stage, then its values
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kRing = kQ8Stages * kStage;
   // shared memory: rings, warp partials, rotated q, barriers
   static constexpr int kPartOff = kQ8Warps * kRing;
   static constexpr int kQOff = kPartOff + kQ8Warps * (D + 4) * 4;
-  static constexpr int kBarOff = kQOff + D * 4;
+  static constexpr int kBarOff = kQOff + kQ8Warps * D * 4;
   static constexpr int kBytes = kBarOff + kQ8Warps * kQ8Stages * 8;
 };
+
+// 2^x of x <= 0: results below 2^-126 are zero, others within two units in the last place.
+__device__ __forceinline__ float exp2_down(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -273,48 +290,12 @@ __device__ __forceinline__ int q8_length(const Q8DecodeArgs& a, int b, bool tell
   return n < 0 ? 0 : (int)cap;
 }
 
-// What a block works on: tiles [t0, t1) of an item (sequence b, head h of n tokens).
+// What a block (or a warp) works on: tiles [t0, t1) of an item, sequence b's head h.
 struct Q8Item {
   int b, h, n, t0, t1;
   int c0, pieces;       // first block with a piece of the item, and how many there are
   int slot, first_slot; // partial slot (of two per block) of this block's and of c0's piece
 };
-
-__device__ __forceinline__ long long q8_div(long long x, int q) {
-  return x >> 32 ? x / q : (long long)((uint32_t)x / (uint32_t)q);
-}
-
-// Sums over the block before this thread and in all, of four ints each (0 <= sums < 2^31).
-struct Int4Scan {
-  int before[4], total[4];
-};
-__device__ __forceinline__ Int4Scan block_scan4(const int* v, int (*sums)[4]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[j] = v[j];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x[j], o);
-      if (lane >= o) x[j] += y;
-    }
-    if (lane == 31) sums[warp][j] = x[j];
-  }
-  __syncthreads();
-  Int4Scan r;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    r.before[j] = x[j] - v[j];
-    r.total[j] = 0;
-#pragma unroll
-    for (int w = 0; w < kQ8Warps; ++w) {
-      if (w < warp) r.before[j] += sums[w][j];
-      r.total[j] += sums[w][j];
-    }
-  }
-  return r;
-}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q8DecodeArgs a) {
@@ -322,151 +303,222 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   constexpr int W = S::kWords;
   extern __shared__ __align__(128) unsigned char sm[];
   float* parts = reinterpret_cast<float*>(sm + S::kPartOff);      // [warps][4 + D]
-  float* qs = reinterpret_cast<float*>(sm + S::kQOff);
-  __shared__ long long sums64[kQ8Warps];
-  __shared__ int sums4[kQ8Warps][4];
-  __shared__ long long start_at;      // units (aligned: pieces) before the first item's sequence
-  __shared__ int start_b;
+  __shared__ uint32_t sums[kQ8Warps];
+  __shared__ int longest[kQ8Warps];
+  __shared__ unsigned long long sums3[kQ8Warps];
+  __shared__ uint32_t start_at[kQ8Warps];   // units (aligned: pieces) before the sequence
+  __shared__ int start_b[kQ8Warps];         // of a block's, or warp's, first item
   __shared__ int abort_word, is_last, told;
-  __shared__ float self_score;
   volatile int* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
   unsigned char* ring = sm + warp * S::kRing;
+  float* qs = reinterpret_cast<float*>(sm + S::kQOff) + warp * D;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff) + warp * kQ8Stages;
 
   // ---------------------------------------------------------------- the block's range
-  // Units: one per tile and head, one for an empty item.  When the grid can give every
-  // item blocks of its own, each block gets one piece of one item (`aligned`: pieces of up
-  // to q tiles, for the least q of four that fits the grid); otherwise range c is
-  // units [c q, c q + q) and may hold the end of one item, whole ones and a beginning.
+  // Units: an item's tiles (one for an empty item) after kQ8ItemBlock or kQ8ItemWarp more
+  // for its start and merge; the host keeps their number below 2^31.  Three ways to divide
+  // them:
+  //   aligned   the grid can give every item blocks of its own: each block gets one piece of
+  //             one item, of up to q tiles, for the least q of three that fits the grid
+  //   ranges    block c gets units [c q, c q + q): the end of one item, whole ones and a
+  //             beginning
+  //   by warp   many short items: each warp gets the items that begin in its range, whole,
+  //             and meets no other warp
+  // The one whose busiest warp has least to do is taken.
   const int per = (a.B + kQ8Threads - 1) / kQ8Threads;
   const int seg0 = min(tid * per, a.B), seg1 = min(seg0 + per, a.B);
-  auto tiles_of = [&](int b, bool tell) {
-    return max(1, (int)(((long long)q8_length(a, b, tell) + S::kTile - 1) / S::kTile));
-  };
-  long long mine = 0;
-  for (int b = seg0; b < seg1; ++b) mine += tiles_of(b, c == 0);
+  auto tiles_of = [&](int n) { return max(1, (int)(((uint32_t)n + S::kTile - 1) / S::kTile)); };
+  uint32_t mine = 0;
+  int most = 0;
+  for (int b = seg0; b < seg1; ++b) {
+    const int tiles = tiles_of(q8_length(a, b, c == 0));
+    mine += tiles;
+    most = max(most, tiles);
+  }
   if (tid == 0) {
     abort_word = 0;
     told = 0;
-    start_b = 0;
-    start_at = 0;
   }
   if (lane == 0) {
     for (int s = 0; s < kQ8Stages; ++s) sm100::mbar_init(&bars[s], 1);
     sm100::fence_mbar_init();
   }
-  long long upto = mine;
+  uint32_t before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += y;
+    const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
   }
-  if (lane == 31) sums64[warp] = upto;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    sums[warp] = before;
+    longest[warp] = most;
+  }
+  before -= mine;
   __syncthreads();
-  long long before = upto - mine, total = 0;
+  uint32_t total = 0;
 #pragma unroll
   for (int w = 0; w < kQ8Warps; ++w) {
-    if (w < warp) before += sums64[w];
-    total += sums64[w];
+    if (w < warp) before += sums[w];
+    total += sums[w];
+    most = max(most, longest[w]);
   }
-  const long long units = total * a.H;
-  int q = max(kQ8MinTiles, (int)q8_div(units + gridDim.x - 1, gridDim.x));
+  const uint32_t H = a.H, items = a.B * H, grid = gridDim.x, warps = grid * kQ8Warps;
+  const uint32_t block_units = (total + a.B * kQ8ItemBlock) * H;
+  const uint32_t warp_units = (total + a.B * kQ8ItemWarp) * H;
+  const uint32_t in_turn = (items + warps - 1) / warps;          // items of one warp
+  const uint32_t warp_cost = min(in_turn * (most + kQ8ItemWarp), warp_units / warps + most);
+  uint32_t block_cost = block_units / warps + kQ8ItemBlock / 2;
+  uint32_t q = 0, blocks = 0, start_pieces = 0, mine_pieces = 0;
   bool aligned = false;
-  int blocks, start_pieces = 0, mine_pieces = 0;
-  if ((long long)a.B * a.H <= gridDim.x) {
-    int qj[4], v[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) qj[j] = q + (q * j + 3) / 4;
+  if (items <= grid) {
+    // pieces for three q, in fields of 21 bits: at most 444 sequences of 445 pieces
+    const uint32_t q0 = max((uint32_t)kQ8MinTiles, (total * H + grid - 1) / grid);
+    unsigned long long v = 0;
     for (int b = seg0; b < seg1; ++b) {
-      const int tiles = tiles_of(b, false);
+      const uint32_t tiles = tiles_of(q8_length(a, b, false));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += min((tiles + qj[j] - 1) / qj[j], (int)gridDim.x + 1);
-    }
-    const Int4Scan sc = block_scan4(v, sums4);
-#pragma unroll
-    for (int j = 3; j >= 0; --j)
-      if ((long long)sc.total[j] * a.H <= gridDim.x) {
-        aligned = true;
-        q = qj[j];
-        blocks = sc.total[j] * a.H;
-        start_pieces = sc.before[j];
-        mine_pieces = v[j];
+      for (int j = 0; j < 3; ++j) {
+        const uint32_t qj = q0 + j * kQ8ItemBlock / 2;
+        v += (unsigned long long)min((tiles + qj - 1) / qj, grid + 1) << (21 * j);
       }
+    }
+    unsigned long long upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) sums3[warp] = upto;
+    __syncthreads();
+    unsigned long long all = 0;
+    upto -= v;
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) {
+      if (w < warp) upto += sums3[w];
+      all += sums3[w];
+    }
+#pragma unroll
+    for (int j = 2; j >= 0; --j) {
+      constexpr uint32_t kField = (1u << 21) - 1;
+      const uint32_t n = (uint32_t)(all >> (21 * j)) & kField;
+      if (n * H <= grid) {
+        aligned = true;
+        q = q0 + j * kQ8ItemBlock / 2;
+        blocks = n * H;
+        start_pieces = (uint32_t)(upto >> (21 * j)) & kField;
+        mine_pieces = (uint32_t)(v >> (21 * j)) & kField;
+      }
+    }
+    if (aligned) block_cost = min(q, (uint32_t)most) / kQ8Warps + kQ8ItemBlock / 4;
   }
-  if (!aligned) blocks = (int)q8_div(units + q - 1, q);
+  const bool by_warp = warp_cost < block_cost;
+  const uint32_t units = by_warp ? warp_units : block_units;
+  if (by_warp) {
+    aligned = false;
+    q = (units + warps - 1) / warps;
+    blocks = (units + kQ8Warps * q - 1) / (kQ8Warps * q);
+  } else if (!aligned) {
+    q = max((uint32_t)kQ8MinTiles, (units + grid - 1) / grid);
+    blocks = (units + q - 1) / q;
+  }
   if (c >= blocks) return;
+  const uint32_t extra = by_warp ? kQ8ItemWarp : kQ8ItemBlock;   // an item's units before its tiles
+  const int team = by_warp ? c * kQ8Warps + warp : c;
+  const int step = by_warp ? 1 : kQ8Warps, lead = by_warp ? 0 : warp;   // a warp's tiles
   {
-    const long long x = aligned ? c : (long long)c * q;
-    long long at = (aligned ? start_pieces : before) * a.H;
-    if (x >= at && x < at + (aligned ? mine_pieces : mine) * a.H) {
+    // the sequence that the block's (or each warp's) first unit lies in
+    const int teams = by_warp ? kQ8Warps : 1;
+    const uint32_t at0 = (aligned ? start_pieces : before + seg0 * extra) * H;
+    const uint32_t end0 = at0 + (aligned ? mine_pieces : mine + (seg1 - seg0) * extra) * H;
+    for (int w = 0; w < teams; ++w) {
+      const uint32_t x = aligned ? c : (c * teams + w) * q;
+      if (x < at0 || x >= end0) continue;
+      uint32_t at = at0;
       int b = seg0;
-      for (; b < seg1; ++b) {
-        const int tiles = tiles_of(b, false);
-        const long long len = (long long)(aligned ? (tiles + q - 1) / q : tiles) * a.H;
+      for (; b < seg1 - 1; ++b) {
+        const uint32_t tiles = tiles_of(q8_length(a, b, false));
+        const uint32_t len = (aligned ? (tiles + q - 1) / q : tiles + extra) * H;
         if (x < at + len) break;
         at += len;
       }
-      start_b = b;
-      start_at = at;
+      start_b[w] = b;
+      start_at[w] = at;
     }
   }
   __syncthreads();
 
   // ---------------------------------------------------------------- its items
-  const int r = lane >> 3, col = lane & 7;          // token row of a group of four, dims' eighth
+  const int r = lane / S::kLanes, col = lane % S::kLanes;      // row of a load, its dims
   uint32_t used = 0;                                // tiles this warp has put through its ring
   bool aborted = false;
-  long long seq_at = start_at, u = (long long)c * q;   // range: first unit of sequence b, next unit
-  const long long u1 = min(u + q, units);
+  uint32_t u = team * q;                            // next unit
+  const uint32_t u1 = min(u + q, units);
+  const int at_w = by_warp ? warp : 0;
+  uint32_t seq_at = start_at[at_w];                 // first unit (piece) of sequence it.b
   Q8Item it;
-  it.b = start_b;
-  // the item that unit u lies in (range), or the block's piece (aligned)
+  it.b = start_b[at_w];
+  // the item that unit u lies in, or the block's piece (aligned); false: there is none
   auto find_item = [&]() {
     if (aligned) {
       it.n = q8_length(a, it.b, false);
-      const int tiles = tiles_of(it.b, false), pieces = (tiles + q - 1) / q;
-      const int k = c - (int)seq_at;
+      const uint32_t tiles = tiles_of(it.n), pieces = (tiles + q - 1) / q, k = c - seq_at;
       it.h = k / pieces;
-      const int part = k - it.h * pieces, base = tiles / pieces, rem = tiles - base * pieces;
+      const uint32_t part = k - it.h * pieces, base = tiles / pieces, rem = tiles - base * pieces;
       it.t0 = part * base + min(part, rem);
       it.t1 = it.t0 + base + (part < rem ? 1 : 0);
       it.c0 = c - part;
       it.pieces = pieces;
       it.slot = it.first_slot = 0;
-      return;
+      return true;
     }
-    int tiles;
-    for (;;) {
-      it.n = q8_length(a, it.b, false);
-      tiles = tiles_of(it.b, false);
-      if (u < seq_at + (long long)tiles * a.H) break;
-      seq_at += (long long)tiles * a.H;
-      ++it.b;
+    while (u < u1) {
+      uint32_t len;
+      for (;;) {
+        it.n = q8_length(a, it.b, false);
+        len = tiles_of(it.n) + extra;
+        if (u < seq_at + len * H) break;
+        seq_at += len * H;
+        ++it.b;
+      }
+      it.h = (u - seq_at) / len;
+      const uint32_t item0 = seq_at + it.h * len, tile0 = item0 + extra;
+      if (by_warp) {
+        const bool begun = u > item0;               // in the range before this one
+        u = item0 + len;
+        if (begun) continue;
+        it.t0 = 0;
+        it.t1 = len - extra;
+        it.pieces = 1;
+        return true;
+      }
+      const uint32_t end = min(item0 + len, u1);
+      it.t0 = u > tile0 ? u - tile0 : 0;
+      it.t1 = end > tile0 ? end - tile0 : 0;
+      u = end;
+      if (it.t0 == it.t1) continue;                 // its tiles are all in the next range
+      it.c0 = tile0 / q;
+      it.pieces = (item0 + len - 1) / q - it.c0 + 1;
+      // slot 0: the first item of a block's range, slot 1: a later one, which is its last
+      it.slot = item0 <= c * q ? 0 : 1;
+      it.first_slot = item0 <= it.c0 * q ? 0 : 1;
+      return true;
     }
-    it.h = (int)q8_div(u - seq_at, tiles);
-    const long long item0 = seq_at + (long long)it.h * tiles;
-    it.t0 = (int)(u - item0);
-    it.t1 = (int)min((long long)tiles, u1 - item0);
-    it.c0 = (int)q8_div(item0, q);
-    it.pieces = (int)q8_div(item0 + tiles - 1, q) - it.c0 + 1;
-    // slot 0: the first item of a block's range, slot 1: a later one, which is its last
-    it.slot = u == (long long)c * q ? 0 : 1;
-    it.first_slot = (long long)it.c0 * q == item0 ? 0 : 1;
-    u = item0 + it.t1;
+    return false;
   };
 
-  // Lane g < kGroups looks after group g of each tile: its page id (loaded two tiles
-  // ahead of the tile's use), its copies, its scales (loaded one tile ahead).
+  // Lane g < kParts looks after block g of each tile: its page id (loaded two tiles ahead of
+  // the tile's use), its copies, its scales (loaded one tile ahead).
   const size_t page_step = (size_t)a.H << a.shift;             // rows per page, all heads
   bool bad = false;
-  auto group_id = [&](int t) {
-    if (lane >= S::kGroups || t >= it.t1) return -1;
+  auto part_id = [&](int t) {
+    if (lane >= S::kParts || t >= it.t1) return -1;
     const int tok = t * S::kTile + lane * 16;                  // lengths stay below 2^31
     return tok < it.n ? __ldg(a.block_table + (long long)it.b * a.max_pages + (tok >> a.shift)) : -1;
   };
   auto checked = [&](int t, int id) {                          // -1 for what is not there
-    const bool there = lane < S::kGroups && t < it.t1 && t * S::kTile + lane * 16 < it.n;
+    const bool there = lane < S::kParts && t < it.t1 && t * S::kTile + lane * 16 < it.n;
     const bool ok = there && id >= 0 && id < a.n_pages;
     bad |= there && !ok;
     return ok ? id : -1;
@@ -475,117 +527,134 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     if (t >= it.t1) return;
     const int s = seq % kQ8Stages;
     const unsigned live = __ballot_sync(0xffffffffu, id >= 0);
-    if (lane == 0) sm100::mbar_arrive_expect_tx(&bars[s], __popc(live) * 2 * S::kGroupBytes);
+    if (lane == 0) sm100::mbar_arrive_expect_tx(&bars[s], __popc(live) * 2 * S::kPartBytes);
     __syncwarp();
     if (id >= 0) {
       const int tok = t * S::kTile + lane * 16;
       const size_t run = (id * page_step + ((size_t)it.h << a.shift) +
                           (tok & ((1 << a.shift) - 1))) * D;
-      unsigned char* st = ring + s * S::kStage + lane * S::kGroupBytes;
-      sm100::bulk_load(st, a.kc + run, S::kGroupBytes, &bars[s]);
-      sm100::bulk_load(st + S::kHalf, a.vc + run, S::kGroupBytes, &bars[s]);
+      unsigned char* st = ring + s * S::kStage + lane * S::kPartBytes;
+      sm100::bulk_load(st, a.kc + run, S::kPartBytes, &bars[s]);
+      sm100::bulk_load(st + S::kHalf, a.vc + run, S::kPartBytes, &bars[s]);
     }
   };
   auto scale_of = [&](const float* scales, int id) {
     return id >= 0 ? __ldg(scales + (size_t)id * a.H + it.h) : 0.f;
   };
-  int id0 = -1, id1 = -1, id2 = -1;                            // tiles t, t + 4, t + 8
+  int id0 = -1, id1 = -1, id2 = -1;                            // a warp's next three tiles
   float ks0 = 0.f, vs0 = 0.f;
-  auto start_item = [&]() {
-    const int first = it.t0 + warp;
-    id0 = group_id(first);
-    id1 = group_id(first + kQ8Warps);
-    id2 = group_id(first + 2 * kQ8Warps);
+  auto load_ids = [&]() {
+    const int first = it.t0 + lead;
+    id0 = part_id(first);
+    id1 = part_id(first + step);
+    id2 = part_id(first + 2 * step);
+  };
+  auto start_copies = [&]() {
+    const int first = it.t0 + lead;
     id0 = checked(first, id0);
-    id1 = checked(first + kQ8Warps, id1);
+    id1 = checked(first + step, id1);
     if (!aborted) {
       issue(first, id0, used);
-      issue(first + kQ8Warps, id1, used + 1);
+      issue(first + step, id1, used + 1);
     }
     ks0 = scale_of(a.ks, id0);
     vs0 = scale_of(a.vs, id0);
   };
-  find_item();
-  start_item();
-  for (bool more = true; more;) {
-    const int first = it.t0 + warp;
+  bool more = find_item(), started = false;
+  unsigned finished = 0;                                       // blocks that finished before
+  auto finish_block = [&]() {
+    if (told || c == 0) __threadfence();                       // block 0 tells of lengths
+    return atomicAdd(a.counter, 1u);
+  };
+  if (more) load_ids();
+  while (more) {
+    const int first = it.t0 + lead;
     const size_t bh = (size_t)it.b * a.H + it.h;
 
-    // q rotated at q_pos, into shared memory; the in-flight token's score, which needs no
-    // rotation, both sitting at q_pos
-    float v_own = 0.f;
-    if (tid < 32) {
-      float acc = 0.f;
-      if (tid < D / 8) {
-        const bool turn = a.rope != nullptr;
-        const RowChunk rc = row_chunk(tid, D, a.rd, turn ? a.layout : LLA_ROPE_INTERLEAVED);
-        float v[8], k[8];
+    // q rotated at q_pos, through shared memory, by each warp for itself; the in-flight
+    // token's score, which needs no rotation, both sitting at q_pos
+    float self = 0.f;
+    {
+      const bool turn = a.rope != nullptr;
+      const RowChunk rc = row_chunk(lane, D, a.rd, turn ? a.layout : LLA_ROPE_INTERLEAVED);
+      float v[8], k[8];
+      int asked = 0;
+      if (lane < D / 8) {
+        if (turn) asked = a.q_pos[it.b];
         load_chunk(static_cast<const T*>(a.q) + bh * D, rc, v);
+        if (a.k_self) load_chunk(static_cast<const T*>(a.k_self) + bh * D, rc, k);
+      }
+      if (!started) start_copies();
+      started = true;
+      if (lane < D / 8) {
         if (a.k_self) {
-          load_chunk(static_cast<const T*>(a.k_self) + bh * D, rc, k);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc = fmaf(v[j], k[j], acc);
+          for (int j = 0; j < 8; ++j) self = fmaf(v[j], k[j], self);
         }
         if (turn) {
-          const int pos = checked_position(a.q_pos[it.b], a.rope_max_pos, nullptr, false);
-          if (tid == 0 && pos != a.q_pos[it.b]) {
+          const int pos = checked_position(asked, a.rope_max_pos, nullptr, false);
+          if (lane == 0 && pos != asked) {
             atomicOr(a.status, LLA_STATUS_POSITION_RANGE);
             told = 1;
           }
           rotate_chunk(a.rope + (size_t)pos * (a.rd / 2), rc, 1.f, v);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          qs[rc.lo + j] = v[j];
-          qs[rc.hi + j] = v[4 + j];
-        }
+        store4(qs + rc.lo, v);
+        store4(qs + rc.hi, v + 4);
       }
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-      if (tid == 0) self_score = acc * a.kappa;
     }
-    if (a.k_self && tid < D) v_own = as_float(static_cast<const T*>(a.v_self)[bh * D + tid]);
-    __syncthreads();
-    // this lane's dims as three signed digits of 7 bits, the largest |q| at 127 * 2^14
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) self += __shfl_xor_sync(0xffffffffu, self, off);
+    self *= a.kappa;
+    __syncwarp();
+
+    // q as three signed digits of 7 bits, the largest |q| at 127 * 2^14: a lane splits four
+    // dims and takes the words of its own through shared memory
     uint32_t q1[W], q2[W], q3[W];
     float score_scale;
     bool strange = false;                                       // a NaN or an infinity in q
     {
-      float v[4 * W], amax = 0.f;
+      float v[4] = {0.f, 0.f, 0.f, 0.f}, amax = 0.f;
+      if (lane < D / 4) load4(qs + 4 * lane, v);
 #pragma unroll
-      for (int j = 0; j < 4 * W; ++j) {
-        v[j] = qs[col * 4 * W + j];
+      for (int j = 0; j < 4; ++j) {
         amax = fmaxf(amax, fabsf(v[j]));
         strange |= !(fabsf(v[j]) <= FLT_MAX);
       }
-      strange = __any_sync(0xffffffffu, strange);
+      strange = __any_sync(0xffffffffu, strange);               // and the values are read
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       constexpr float kTop = 127.f * 16384.f;
       const float inv = amax > kQ8Tiny ? kTop / amax : 0.f;
       score_scale = strange ? 0.f : a.kappa * amax / kTop;      // strange: pl becomes NaN below
+      uint32_t hi = 0, mid = 0, lo = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int x = __float2int_rn(v[j] * inv), y = (x + 64) >> 7, z = (y + 64) >> 7;
+        lo |= (uint32_t)((x - (y << 7)) & 255) << (8 * j);      // -64 .. 63
+        mid |= (uint32_t)((y - (z << 7)) & 255) << (8 * j);
+        hi |= (uint32_t)(z & 255) << (8 * j);                   // -127 .. 127
+      }
+      uint32_t* words = reinterpret_cast<uint32_t*>(qs);
+      if (lane < D / 4) {
+        words[lane] = hi;
+        words[D / 4 + lane] = mid;
+        words[D / 2 + lane] = lo;
+      }
+      __syncwarp();
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        q1[w] = q2[w] = q3[w] = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          int x = __float2int_rn(v[4 * w + j] * inv);
-          const int lo = ((x + 64) & 127) - 64;
-          x = (x - lo) >> 7;
-          const int mid = ((x + 64) & 127) - 64;
-          x = (x - mid) >> 7;
-          q1[w] |= (uint32_t)(x & 255) << (8 * j);
-          q2[w] |= (uint32_t)(mid & 255) << (8 * j);
-          q3[w] |= (uint32_t)(lo & 255) << (8 * j);
-        }
+        q1[w] = words[col * W + w];
+        q2[w] = words[D / 4 + col * W + w];
+        q3[w] = words[D / 2 + col * W + w];
       }
     }
 
     // Sums are relative to 2^m, m the largest score so far: l of 2^(s - m), o of
-    // 2^(s - m) v.  acc holds weights w = 2^(s - m) vs / R * (2^24 - 1) times codes, R
+    // 2^(s - m) v.  acc holds weights w = 2^(s - m) vs / R * kQ8Weight times codes, R
     // the reference that no weight since the last flush exceeds.  A larger weight flushes
     // acc into o; a larger score rescales l, o and R.
-    float m = -INFINITY, l = 0.f, R = 0.f, wf = 0.f;             // wf = (2^24 - 1) / R
+    float m = -INFINITY, l = 0.f, R = 0.f, wf = 0.f;             // wf = kQ8Weight / R
     float o[4 * W];
     int acc1[4 * W], acc2[4 * W], acc3[4 * W];
 #pragma unroll
@@ -593,8 +662,11 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       o[j] = 0.f;
       acc1[j] = acc2[j] = acc3[j] = 0;
     }
-    int groups = 0;
+    int since = 0;                                               // tiles since the last flush
+    bool held = false;                                           // acc holds something
     auto flush = [&]() {
+      if (!held) return;
+      held = false;
       const float f = R * (1.f / kQ8Weight);
 #pragma unroll
       for (int j = 0; j < 4 * W; ++j) {
@@ -602,21 +674,24 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
                     o[j]);
         acc1[j] = acc2[j] = acc3[j] = 0;
       }
-      groups = 0;
+      since = 0;
     };
 
-    const int i_own = ((col >> 1) & 1) | ((col >> 1) & 2);      // row group this lane ends up with
+    // Rows r + kRows i of a group are a lane's, i = 0 .. 3; it ends up with the scores of
+    // i_own (and i_own + 1 when it has two).
+    const int i_own = S::kLanes == 8 ? (((col >> 1) & 1) | ((col >> 1) & 2))
+                                     : S::kLanes == 4 ? (((col & 1)) | (col & 2)) : 2 * col;
     uint32_t seq = used;
-    for (int t = first; t < it.t1 && !aborted; t += kQ8Warps, ++seq) {
+    for (int t = first; t < it.t1 && !aborted; t += step, ++seq) {
       const int s = seq % kQ8Stages;
       const unsigned live = __ballot_sync(0xffffffffu, id0 >= 0);
       // scales of the next tile, page ids of the one after it
       const float ks1 = scale_of(a.ks, id1), vs1 = scale_of(a.vs, id1);
-      id2 = checked(t + 2 * kQ8Warps, id2);
-      const int id3 = group_id(t + 3 * kQ8Warps);
+      id2 = checked(t + 2 * step, id2);
+      const int id3 = part_id(t + 3 * step);
       if (!sm100::mbar_wait(&bars[s], (seq / kQ8Stages) & 1u, abort_flag)) {
         // copies already issued land before the block can end
-        for (int k = 0; k < kQ8Stages && t + k * kQ8Warps < it.t1; ++k) {
+        for (int k = 0; k < kQ8Stages && t + k * step < it.t1; ++k) {
           const unsigned long long w0 = sm100::global_timer_ns();
           while (!sm100::mbar_try_wait(&bars[(seq + k) % kQ8Stages], ((seq + k) / kQ8Stages) & 1u) &&
                  sm100::global_timer_ns() - w0 < sm100::kWaitTimeoutNs) {
@@ -625,19 +700,18 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
         aborted = true;
         break;
       }
+      if (++since >= kQ8FlushTiles) flush();
       const unsigned char* st = ring + s * S::kStage + r * D + col * 4 * W;
-      const int rows_left = it.n - t * S::kTile - r - 4 * i_own;   // of this lane's row of group 0
+      const int rows_left = it.n - t * S::kTile - r - S::kRows * i_own;   // of a lane's first score
 #pragma unroll
-      for (int g = 0; g < S::kGroups; ++g) {
-        if (!(live >> g & 1)) continue;                         // warp-uniform
-        const float ksc = __shfl_sync(0xffffffffu, ks0, g) * score_scale;
-        const float vsc = __shfl_sync(0xffffffffu, vs0, g);
-        const unsigned char* kp = st + g * S::kGroupBytes;
+      for (int g = 0; g < 2; ++g) {
+        if (!(live >> (g * S::kSubs) & ((1 << S::kSubs) - 1))) continue;  // warp-uniform
+        const unsigned char* kp = st + g * S::kSubs * S::kPartBytes;
         float part[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t kw[W];
-          load_words<W>(kp + i * 4 * D, kw);
+          load_words<W>(kp + i * S::kRows * D, kw);
           int s1 = 0, s2 = 0, s3 = 0;
 #pragma unroll
           for (int w = 0; w < W; ++w) {
@@ -647,20 +721,38 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
           }
           part[i] = fmaf((float)(s1 * 128 + s2), 128.f, (float)s3);
         }
-        // sum over the row's eight lanes; a lane keeps row r + 4 i_own
-        float x0 = (col & 4 ? part[2] : part[0]) +
-                   __shfl_xor_sync(0xffffffffu, col & 4 ? part[0] : part[2], 4);
-        const float x1 = (col & 4 ? part[3] : part[1]) +
-                         __shfl_xor_sync(0xffffffffu, col & 4 ? part[1] : part[3], 4);
-        x0 = (col & 2 ? x1 : x0) + __shfl_xor_sync(0xffffffffu, col & 2 ? x0 : x1, 2);
-        x0 += __shfl_xor_sync(0xffffffffu, x0, 1);
-        const float sc = rows_left > 16 * g ? x0 * ksc : -INFINITY;
-        if (__any_sync(0xffffffffu, sc > m)) {
-          float mt = sc;
+        // sums over a row's lanes, each exchange halving what a lane holds
+        constexpr int kFar = S::kLanes / 2, kNear = S::kLanes / 4;
+        const bool upper = col & kFar;
+        float x[2];
+        x[0] = (upper ? part[2] : part[0]) +
+               __shfl_xor_sync(0xffffffffu, upper ? part[0] : part[2], kFar);
+        x[1] = (upper ? part[3] : part[1]) +
+               __shfl_xor_sync(0xffffffffu, upper ? part[1] : part[3], kFar);
+        if constexpr (S::kLanes >= 4) {
+          const bool odd = col & kNear;
+          x[0] = (odd ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], kNear);
+        }
+        if constexpr (S::kLanes == 8) x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+        float sc[S::kScores], vsc[S::kScores];
+        bool above = false, heavy = false;
 #pragma unroll
-          for (int off = 2; off < 32; off <<= 1)
+        for (int k = 0; k < S::kScores; ++k) {
+          // the 16-token block of the group that the row lies in
+          const int sub = g * S::kSubs + (S::kSubs == 1 ? 0 : S::kSubs == 2 ? i_own >> 1 : i_own + k);
+          const float ksc = __shfl_sync(0xffffffffu, ks0, sub) * score_scale;
+          vsc[k] = __shfl_sync(0xffffffffu, vs0, sub);
+          const bool there = rows_left > g * S::kGroup + k * S::kRows && (live >> sub & 1);
+          sc[k] = there ? x[k] * ksc : -INFINITY;
+          above |= sc[k] > m;
+          heavy |= vsc[k] > R;                                  // weights are at most vs: p <= 1
+        }
+        if (__any_sync(0xffffffffu, above)) {
+          float mt = S::kScores == 2 ? fmaxf(sc[0], sc[S::kScores - 1]) : sc[0];
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1)
             mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-          const float f = exp2f(m - mt);                        // 0 the first time
+          const float f = exp2_down(m - mt);                    // 0 the first time
           m = mt;
           l *= f;
           R *= f;
@@ -671,30 +763,46 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
             R = kQ8SmallRef;
           }
           wf = kQ8Weight / R;
+          heavy = true;
         }
-        const float p = exp2f(sc - m);
-        l += col & 1 ? 0.f : p;
-        if (vsc > R || groups >= kQ8FlushGroups) {              // p <= 1
-          flush();
-          R = fmaxf(R, vsc);
-          wf = kQ8Weight / R;
+        if (__any_sync(0xffffffffu, heavy)) {
+          float top = S::kScores == 2 ? fmaxf(vsc[0], vsc[S::kScores - 1]) : vsc[0];
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          if (top > R) {
+            flush();
+            R = top;
+            wf = kQ8Weight / R;
+          }
         }
-        ++groups;
-        const uint32_t wt = __float2uint_rn(fminf(p * (vsc * wf), kQ8Weight));
-        // the four rows' weights, then their bytes: hi, mid, lo words of four tokens
-        const uint32_t w2 = __shfl_xor_sync(0xffffffffu, wt, 2);
-        const uint32_t e0 = col & 2 ? w2 : wt, e1 = col & 2 ? wt : w2;
-        const uint32_t f0 = __shfl_xor_sync(0xffffffffu, e0, 4);
-        const uint32_t f1 = __shfl_xor_sync(0xffffffffu, e1, 4);
-        const uint32_t g0 = col & 4 ? f0 : e0, g1 = col & 4 ? f1 : e1;
-        const uint32_t g2 = col & 4 ? e0 : f0, g3 = col & 4 ? e1 : f1;
+        uint32_t wt[S::kScores];
+#pragma unroll
+        for (int k = 0; k < S::kScores; ++k) {
+          const float p = exp2_down(sc[k] - m);
+          l += p;
+          wt[k] = __float2uint_rn(p * (vsc[k] * wf));
+        }
+        // the weights of a lane's four rows, then their bytes: hi, mid, lo words of four tokens
+        uint32_t e0 = wt[0], e1 = wt[S::kScores - 1];
+        if constexpr (S::kLanes >= 4) {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, wt[0], kNear);
+          const bool odd = col & kNear;
+          e0 = odd ? other : wt[0];
+          e1 = odd ? wt[0] : other;
+        }
+        const uint32_t f0 = __shfl_xor_sync(0xffffffffu, e0, kFar);
+        const uint32_t f1 = __shfl_xor_sync(0xffffffffu, e1, kFar);
+        const uint32_t g0 = upper ? f0 : e0, g1 = upper ? f1 : e1;
+        const uint32_t g2 = upper ? e0 : f0, g3 = upper ? e1 : f1;
         const uint32_t a01 = __byte_perm(g0, g1, 0x5140), a23 = __byte_perm(g2, g3, 0x5140);
         const uint32_t h01 = __byte_perm(g0, g1, 0x0062), h23 = __byte_perm(g2, g3, 0x0062);
         const uint32_t wlo = __byte_perm(a01, a23, 0x5410), wmid = __byte_perm(a01, a23, 0x7632);
         const uint32_t whi = __byte_perm(h01, h23, 0x5410);
+        held = true;
         uint32_t vw[4][W];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_words<W>(kp + S::kHalf + i * 4 * D, vw[i]);
+        for (int i = 0; i < 4; ++i) load_words<W>(kp + S::kHalf + i * S::kRows * D, vw[i]);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           // four rows of four dims, turned into four dims of four rows
@@ -713,37 +821,67 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
         }
       }
       __syncwarp();                                             // the stage is read
-      issue(t + kQ8Stages * kQ8Warps, id2, seq + kQ8Stages);
+      issue(t + kQ8Stages * step, id2, seq + kQ8Stages);
       id0 = id1;
       id1 = id2;
       id2 = id3;
       ks0 = ks1;
       vs0 = vs1;
     }
-    if (it.t1 > first) used += (it.t1 - first + kQ8Warps - 1) / kQ8Warps;
+    if (it.t1 > first) used += (it.t1 - first + step - 1) / step;
     if (__any_sync(0xffffffffu, bad) && lane == 0) {
       atomicOr(a.status, LLA_STATUS_PAGE_RANGE);
       told = 1;
     }
     bad = false;
+    if (aborted && lane == 0) {
+      atomicOr(a.status, LLA_STATUS_TIMEOUT);
+      told = 1;
+    }
     // the next item's first tiles are on their way while this one is merged
     const Q8Item now = it;
-    more = !aligned && u < u1;
+    more = !aligned && find_item();
     if (more) {
-      find_item();
-      start_item();
+      load_ids();
+      start_copies();
     }
 
     // ---------------------------------------------------------------- merge the warps
     flush();
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    l += __shfl_xor_sync(0xffffffffu, l, 4);
+    if (S::kLanes == 8) l *= 0.5f;                              // two lanes held every score
 #pragma unroll
-    for (int off = 8; off < 32; off <<= 1) {
+    for (int off = 1; off < 32; off <<= 1) {
       l += __shfl_xor_sync(0xffffffffu, l, off);
+      if (off < S::kLanes) continue;
 #pragma unroll
       for (int j = 0; j < 4 * W; ++j) o[j] += __shfl_xor_sync(0xffffffffu, o[j], off);
     }
+    if (by_warp) {
+      float f = 1.f, fs = 0.f;
+      if (a.k_self) {
+        const float top = fmaxf(m, self);
+        f = m > -INFINITY ? exp2f(m - top) : 0.f;
+        fs = exp2f(self - top);
+      }
+      l = fmaf(l, f, fs);
+      if (strange && l != 0.f) l = NAN;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (r == 0) {
+        const size_t at = bh * D + col * 4 * W;
+#pragma unroll
+        for (int j = 0; j < 4 * W; j += 4) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          if (a.k_self) load4(static_cast<const T*>(a.v_self) + at + j, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = l == 0.f ? 0.f : (a.k_self ? fmaf(o[j + i], f, fs * v[i]) : o[j + i]) * inv;
+          store4(static_cast<T*>(a.out) + at + j, v);
+        }
+      }
+      continue;
+    }
+    float v_own = 0.f;
+    if (a.k_self && tid < D) v_own = as_float(static_cast<const T*>(a.v_self)[bh * D + tid]);
     float* pw = parts + warp * (D + 4);
     if (r == 0) {
 #pragma unroll
@@ -754,6 +892,8 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       }
     }
     __syncthreads();
+    // every status bit of the block is told; the count comes back during the merge
+    if (tid == 0 && !more) finished = finish_block();
     float pm = -INFINITY, pl = 0.f, po = 0.f;
 #pragma unroll
     for (int w = 0; w < kQ8Warps; ++w) pm = fmaxf(pm, parts[w * (D + 4)]);
@@ -817,7 +957,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     }
     if (finish) {
       if (a.k_self) {
-        const float self = self_score, top = fmaxf(pm, self);
+        const float top = fmaxf(pm, self);
         const float f = pm > -INFINITY ? exp2f(pm - top) : 0.f, fs = exp2f(self - top);
         pl = fmaf(pl, f, fs);
         po = fmaf(po, f, fs * v_own);
@@ -825,21 +965,17 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       if (strange && pl != 0.f) pl = NAN;
       if (tid < D) put(static_cast<T*>(a.out) + bh * D + tid, pl == 0.f ? 0.f : po / pl);
     }
-    __syncthreads();                                            // parts, qs and is_last are free
-  }
-  if (aborted && lane == 0) {
-    atomicOr(a.status, LLA_STATUS_TIMEOUT);
-    told = 1;
+    __syncthreads();                                            // parts and is_last are free
   }
   // the last block to finish publishes the call's status word and re-arms the counter
-  __syncthreads();
-  if (tid == 0) {
-    if (told || c == 0) __threadfence();                        // block 0 tells of lengths
-    if (atomicAdd(a.counter, 1u) == (unsigned)blocks - 1) {
-      __threadfence();
-      a.status[1] = atomicExch(&a.status[0], 0);
-      atomicExch(a.counter, 0u);
-    }
+  if (by_warp || !started) {                                   // also a range without a tile
+    __syncthreads();
+    if (tid == 0) finished = finish_block();
+  }
+  if (tid == 0 && finished == blocks - 1) {
+    __threadfence();
+    a.status[1] = atomicExch(&a.status[0], 0);
+    atomicExch(a.counter, 0u);
   }
 }
 

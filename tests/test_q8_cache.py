@@ -407,7 +407,10 @@ def test_decode_shared_prefix_and_scale():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,H,n", [(1, 1, 40000), (2, 16, 9000), (300, 2, 200)])
+@pytest.mark.parametrize("B,H,n", [
+    (1, 1, 40000), (2, 16, 9000), (300, 2, 200),      # an item cut into many pieces, many items
+    (1000, 3, 70),                                    # items whole to a warp each
+    (120, 16, 600), (40, 12, 1500)])                  # ranges that begin and end inside items
 def test_decode_many_splits_and_many_sequences(B, H, n):
     g = np.random.default_rng(n)
     lens = np.maximum(1, (n * g.random(B) ** 2).astype(int))
