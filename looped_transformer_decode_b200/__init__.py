@@ -94,10 +94,9 @@ def rope_table(cfg: Cfg, max_pos: int, device="cuda", out=None, scaling: RopeSca
         rd = cfg.d_rope or cfg.d_head                 # rotary dims
         out = torch.empty((max_pos, rd // 2, 2), dtype=torch.float32, device=device)
     if scaling is not None:
-        with torch.cuda.device(out.device):
-            check(lib.lla_rope_table_scaled(ctypes.byref(c), ctypes.byref(scaling.c()), max_pos,
-                                            _ptr(out, torch.float32, "table"), out.numel() * 4,
-                                            _stream()))
+        dev = _device(out)
+        _call(lib.lla_rope_table_scaled, dev, cfg.ref, ctypes.byref(scaling.c()), max_pos,
+              _dense(out, torch.float32, dev, "table"), out.numel() * 4)
         return out
     check(lib.lla_rope_table(ctypes.byref(c), max_pos, _ptr(out, torch.float32, "table"),
                              out.numel() * 4, _stream()))
@@ -265,9 +264,83 @@ def full_decode_attn(cfg: Cfg, rope, ctx_len, q, k_self, v_self, q_pos, k_full, 
     return out
 
 
-# ---------------------------------------------------------------- rotary positions
+# ---------------------------------------------------------------- lean argument passing
+#
+# A decode step makes these calls for every layer and loop, so the checks below cost a few
+# attribute reads per tensor; the detailed message is put together only when one fails.
 
-_ROW_TYPES = {torch.float32: F32, torch.bfloat16: BF16}
+_F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+_ROW_TYPES = {_F32: F32, _BF16: BF16}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _device(t) -> int:
+    """CUDA device index of the tensor whose device the call runs on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    return t.get_device()
+
+
+def _call(fn, dev: int, *args) -> None:
+    """fn(*args, stream) with ``dev`` current, on its current stream."""
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, _raw_stream(dev))
+    if code:
+        check(code)
+
+
+def _refuse(t, dtype, dev, name, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _dense(t, dtype, dev, name, shape=None) -> int:
+    """Address of a contiguous tensor of this type, device and shape."""
+    try:
+        if (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, dtype, dev, name, shape)
+
+
+def _rows(t, dtype, dev, name, shape) -> int:
+    """Address of rows [n, heads, d] whose heads are contiguous; tokens may be strided."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
+            n, heads, d = shape
+            if n == 0 or t.is_contiguous() or (
+                    t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)):
+                return t.data_ptr()
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+    except AttributeError:
+        pass
+    _refuse(t, dtype, dev, name, shape)
+
+
+def _stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _row_type(t, name: str) -> int:
+    kind = _ROW_TYPES.get(getattr(t, "dtype", None))
+    if kind is None:
+        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
+    return kind
 
 
 def _layout(layout: str) -> int:
@@ -276,52 +349,17 @@ def _layout(layout: str) -> int:
     return ROPE_LAYOUTS[layout]
 
 
-def _same_device(first: torch.Tensor, **others):
-    """Device context of ``first``; every other tensor (None skipped) must live there too."""
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
-        raise ValueError("expected CUDA tensors")
-    for name, t in others.items():
-        if isinstance(t, torch.Tensor) and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
-    return torch.cuda.device(first.device)
-
-
-def _opt(t, dtype, name, shape=None):
-    return None if t is None else _ptr(t, dtype, name, shape)
-
-
-def _rows(t: torch.Tensor, dtype: torch.dtype, name: str, shape):
-    """Pointer and token stride of rows [n, heads, d] whose heads are contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    n, heads, d = t.shape
-    if n and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    stride = t.stride(0) if n > 1 else heads * d
-    return ctypes.c_void_p(t.data_ptr()), stride
-
-
-def _check_table(cfg: Cfg, rope) -> int:
-    """Positions covered by a rope table, whose rows must be cfg's; 0 without one."""
+def _table(cfg: Cfg, rope, dev: int):
+    """(address, positions covered) of a rope table of cfg's rotary dims; (None, 0) without one."""
     if rope is None:
-        return 0
-    rd = cfg.d_rope or cfg.d_head
-    if rope.dim() != 3 or tuple(rope.shape[1:]) != (rd // 2, 2):
-        raise ValueError(f"rope has shape {tuple(rope.shape)}, expected (positions, {rd // 2}, 2)")
-    return rope.shape[0]
+        return None, 0
+    if not isinstance(rope, torch.Tensor) or rope.dim() != 3:
+        raise ValueError("rope must be a table from rope_table, or None")
+    n = rope.shape[0]
+    return _dense(rope, _F32, dev, "rope", (n, (cfg.d_rope or cfg.d_head) // 2, 2)), n
 
 
-def _row_type(t, name: str) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype not in _ROW_TYPES:
-        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
-    return _ROW_TYPES[t.dtype]
-
+# ---------------------------------------------------------------- rotary positions
 
 def rope_apply(cfg: Cfg, rope, positions, x, layout: str = "half", inverse: bool = False, out=None,
                status=None):
@@ -331,19 +369,19 @@ def rope_apply(cfg: Cfg, rope, positions, x, layout: str = "half", inverse: bool
     strided (a slice of a fused projection); ``out`` may be ``x``.  ``inverse=True`` rotates back,
     which is the gradient with respect to x given the gradient of the output.
     """
-    kind = _row_type(x, "x")
-    if x.dim() != 3 or x.shape[2] != cfg.d_head:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected (tokens, heads, {cfg.d_head})")
-    n, heads, _ = x.shape
+    kind, dev = _row_type(x, "x"), _device(x)
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != cfg.d_head:
+        raise ValueError(f"x has shape {tuple(shape)}, expected (tokens, heads, {cfg.d_head})")
+    if rope is None:
+        raise ValueError("rope must be a table from rope_table")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    with _same_device(x, rope=rope, positions=positions, out=out, status=status):
-        xp, xs = _rows(x, x.dtype, "x", x.shape)
-        yp, ys = _rows(out, x.dtype, "out", x.shape)
-        check(lib.lla_rope_apply(ctypes.byref(cfg.c()), _ptr(rope, torch.float32, "rope"),
-                                 _check_table(cfg, rope), _layout(layout), int(inverse), kind, n,
-                                 heads, _ptr(positions, torch.int32, "positions", (n,)), xp, xs,
-                                 yp, ys, _opt(status, torch.int32, "status"), _stream()))
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    tp, tn = _table(cfg, rope, dev)
+    _call(lib.lla_rope_apply, dev, cfg.ref, tp, tn, _layout(layout), 1 if inverse else 0, kind,
+          shape[0], shape[1], _dense(positions, _I32, dev, "positions", shape[:1]),
+          _rows(x, x.dtype, dev, "x", shape), _stride(x), _rows(out, x.dtype, dev, "out", shape),
+          _stride(out), None if status is None else _dense(status, _I32, dev, "status"))
     return out
 
 
@@ -357,27 +395,24 @@ def page_map(page: int, ctx_len, n_new, block_table, free_list, n_free, tok_cap:
     ``n_free`` [1] (all int32) in place.  Returns (tok_start int32 [B + 1], slot int64 [tok_cap],
     positions int32 [tok_cap]) of the appended tokens.
     """
+    dev = _device(ctx_len)
     if block_table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("block_table must be [B, max_pages] and free_list [n_pages]")
     B, max_pages = block_table.shape
-    dev = ctx_len.device
     if tok_start is None:
-        tok_start = torch.empty((B + 1,), dtype=torch.int32, device=dev)
+        tok_start = torch.empty((B + 1,), dtype=_I32, device=ctx_len.device)
     if slot is None:
-        slot = torch.empty((tok_cap,), dtype=torch.int64, device=dev)
+        slot = torch.empty((tok_cap,), dtype=_I64, device=ctx_len.device)
     if positions is None:
-        positions = torch.empty((tok_cap,), dtype=torch.int32, device=dev)
-    i32 = torch.int32
-    with _same_device(ctx_len, n_new=n_new, block_table=block_table, free_list=free_list,
-                      n_free=n_free, tok_start=tok_start, slot=slot, positions=positions,
-                      status=status):
-        check(lib.lla_page_map(
-            B, page, max_pages, free_list.shape[0], _ptr(ctx_len, i32, "ctx_len", (B,)),
-            _ptr(n_new, i32, "n_new", (B,)), _ptr(block_table, i32, "block_table"),
-            _ptr(free_list, i32, "free_list"), _ptr(n_free, i32, "n_free", (1,)), tok_cap,
-            _ptr(tok_start, i32, "tok_start", (B + 1,)),
-            _ptr(slot, torch.int64, "slot", (tok_cap,)),
-            _ptr(positions, i32, "positions", (tok_cap,)), _opt(status, i32, "status"), _stream()))
+        positions = torch.empty((tok_cap,), dtype=_I32, device=ctx_len.device)
+    _call(lib.lla_page_map, dev, B, page, max_pages, free_list.shape[0],
+          _dense(ctx_len, _I32, dev, "ctx_len", (B,)), _dense(n_new, _I32, dev, "n_new", (B,)),
+          _dense(block_table, _I32, dev, "block_table"), _dense(free_list, _I32, dev, "free_list"),
+          _dense(n_free, _I32, dev, "n_free", (1,)), tok_cap,
+          _dense(tok_start, _I32, dev, "tok_start", (B + 1,)),
+          _dense(slot, _I64, dev, "slot", (tok_cap,)),
+          _dense(positions, _I32, dev, "positions", (tok_cap,)),
+          None if status is None else _dense(status, _I32, dev, "status"))
     return tok_start, slot, positions
 
 
@@ -399,13 +434,15 @@ class Q8Cache:
     def n_pages(self) -> int:
         return self.k.shape[0]
 
-    def c(self, cfg: Cfg) -> CQ8Cache:
-        n, page = self.n_pages, self.page
+    def ref(self, cfg: Cfg, dev: int):
+        """ctypes reference to the cache of this configuration on this device."""
+        n, H, page, d = self.k.shape
         shape, rows = (n, cfg.H, page, cfg.d_head), (n, cfg.H)
-        return CQ8Cache(_ptr(self.k, torch.int8, "cache.k", shape),
-                        _ptr(self.v, torch.int8, "cache.v", shape),
-                        _ptr(self.k_scale, torch.float32, "cache.k_scale", rows),
-                        _ptr(self.v_scale, torch.float32, "cache.v_scale", rows), n, page)
+        return ctypes.byref(CQ8Cache(
+            _dense(self.k, torch.int8, dev, "cache.k", shape),
+            _dense(self.v, torch.int8, dev, "cache.v", shape),
+            _dense(self.k_scale, _F32, dev, "cache.k_scale", rows),
+            _dense(self.v_scale, _F32, dev, "cache.v_scale", rows), n, page))
 
 
 def q8_cache_alloc(cfg: Cfg, n_pages: int, page: int, device="cuda") -> Q8Cache:
@@ -413,8 +450,8 @@ def q8_cache_alloc(cfg: Cfg, n_pages: int, page: int, device="cuda") -> Q8Cache:
     shape = (n_pages, cfg.H, page, cfg.d_head)
     return Q8Cache(torch.zeros(shape, dtype=torch.int8, device=device),
                    torch.zeros(shape, dtype=torch.int8, device=device),
-                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
-                   torch.zeros(shape[:2], dtype=torch.float32, device=device))
+                   torch.zeros(shape[:2], dtype=_F32, device=device),
+                   torch.zeros(shape[:2], dtype=_F32, device=device))
 
 
 def q8_append(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, tok_start, positions, k, v,
@@ -425,21 +462,17 @@ def q8_append(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, tok_start, p
     ``tok_start`` as ``page_map`` leaves them.  Keys are rotated by ``rope`` at ``positions`` int32
     [n_tok]; with ``rope=None`` (then ``positions`` may be None) they come rotated.
     """
-    kind = _row_type(k, "k")
-    n, B, max_pages = k.shape[0], block_table.shape[0], block_table.shape[1]
-    i32 = torch.int32
-    with _same_device(k, rope=rope, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
-                      v_scale=cache.v_scale, ctx_len=ctx_len, block_table=block_table,
-                      tok_start=tok_start, positions=positions, v=v, status=status):
-        kp, ks = _rows(k, k.dtype, "k", (n, cfg.H, cfg.d_head))
-        vp, vs = _rows(v, k.dtype, "v", (n, cfg.H, cfg.d_head))
-        check(lib.lla_q8_append(
-            ctypes.byref(cfg.c()), ctypes.byref(cache.c(cfg)), _opt(rope, torch.float32, "rope"),
-            _check_table(cfg, rope), _layout(layout), kind, B, max_pages,
-            _ptr(ctx_len, i32, "ctx_len", (B,)), _ptr(block_table, i32, "block_table"), n,
-            _ptr(tok_start, i32, "tok_start", (B + 1,)),
-            _opt(positions, i32, "positions", (n,)), kp, ks, vp, vs,
-            _opt(status, i32, "status"), _stream()))
+    kind, dev = _row_type(k, "k"), _device(k)
+    B, max_pages = block_table.shape
+    shape = (k.shape[0], cfg.H, cfg.d_head)
+    tp, tn = _table(cfg, rope, dev)
+    _call(lib.lla_q8_append, dev, cfg.ref, cache.ref(cfg, dev), tp, tn, _layout(layout), kind, B,
+          max_pages, _dense(ctx_len, _I32, dev, "ctx_len", (B,)),
+          _dense(block_table, _I32, dev, "block_table"), shape[0],
+          _dense(tok_start, _I32, dev, "tok_start", (B + 1,)),
+          None if positions is None else _dense(positions, _I32, dev, "positions", shape[:1]),
+          _rows(k, k.dtype, dev, "k", shape), _stride(k), _rows(v, k.dtype, dev, "v", shape),
+          _stride(v), None if status is None else _dense(status, _I32, dev, "status"))
 
 
 def q8_read(cfg: Cfg, cache: Q8Cache, slot, k_out=None, v_out=None, status=None):
@@ -447,31 +480,29 @@ def q8_read(cfg: Cfg, cache: Q8Cache, slot, k_out=None, v_out=None, status=None)
 
     A slot outside the cache leaves its row as it was (zeros without ``k_out`` / ``v_out``).
     """
+    dev = _device(slot)
     shape = (slot.shape[0], cfg.H, cfg.d_head)
-    bf = torch.bfloat16
     if k_out is None:
-        k_out = torch.zeros(shape, dtype=bf, device=slot.device)
+        k_out = torch.zeros(shape, dtype=_BF16, device=slot.device)
     if v_out is None:
-        v_out = torch.zeros(shape, dtype=bf, device=slot.device)
-    with _same_device(slot, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
-                      v_scale=cache.v_scale, k_out=k_out, v_out=v_out, status=status):
-        check(lib.lla_q8_read(ctypes.byref(cfg.c()), ctypes.byref(cache.c(cfg)), shape[0],
-                              _ptr(slot, torch.int64, "slot", shape[:1]),
-                              _ptr(k_out, bf, "k_out", shape), _ptr(v_out, bf, "v_out", shape),
-                              _opt(status, torch.int32, "status"), _stream()))
+        v_out = torch.zeros(shape, dtype=_BF16, device=slot.device)
+    _call(lib.lla_q8_read, dev, cfg.ref, cache.ref(cfg, dev), shape[0],
+          _dense(slot, _I64, dev, "slot", shape[:1]), _dense(k_out, _BF16, dev, "k_out", shape),
+          _dense(v_out, _BF16, dev, "v_out", shape),
+          None if status is None else _dense(status, _I32, dev, "status"))
     return k_out, v_out
 
 
 def q8_decode_workspace(cfg: Cfg, B: int, n_cap: int, device="cuda"):
     """Workspace of q8_decode_attn for sequences of up to ``n_cap`` = max_pages * page tokens."""
-    n = lib.lla_q8_decode_workspace_bytes(ctypes.byref(cfg.c()), B, n_cap)
+    n = lib.lla_q8_decode_workspace_bytes(cfg.ref, B, n_cap)
     if n == 0:
         raise LLAError(ERR_UNSUPPORTED, last_error())
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
 def q8_decode_launches(cfg: Cfg, B: int, n_cap: int) -> int:
-    return lib.lla_q8_decode_launches(ctypes.byref(cfg.c()), B, n_cap)
+    return lib.lla_q8_decode_launches(cfg.ref, B, n_cap)
 
 
 def q8_decode_attn(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, q, k_self, v_self, q_pos,
@@ -479,24 +510,22 @@ def q8_decode_attn(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, q, k_se
     """Decode attention over the 8-bit cache; returns out [B, H, d] of q's dtype.
 
     ``q``, ``k_self``, ``v_self`` fp32 or bf16 [B, H, d] before rotation (rotated already with
-    ``rope=None``); ``k_self=v_self=None`` attends over the history alone.
+    ``rope=None``); ``k_self=v_self=None`` attends over the history alone.  Calls that may run at
+    the same time need a workspace each.
     """
-    kind = _row_type(q, "q")
+    kind, dev = _row_type(q, "q"), _device(q)
     B, max_pages = block_table.shape
-    rows = (B, cfg.H, cfg.d_head)
+    rows, dtype = (B, cfg.H, cfg.d_head), q.dtype
     if out is None:
-        out = torch.empty(rows, dtype=q.dtype, device=q.device)
+        out = torch.empty(rows, dtype=dtype, device=q.device)
     if ws is None:
         ws = q8_decode_workspace(cfg, B, max_pages * cache.page, q.device)
-    i32 = torch.int32
-    with _same_device(q, rope=rope, cache=cache.k, cache_v=cache.v, k_scale=cache.k_scale,
-                      v_scale=cache.v_scale, ctx_len=ctx_len, block_table=block_table,
-                      k_self=k_self, v_self=v_self, q_pos=q_pos, out=out, ws=ws):
-        check(lib.lla_q8_decode_attn(
-            ctypes.byref(cfg.c()), ctypes.byref(cache.c(cfg)), _opt(rope, torch.float32, "rope"),
-            _check_table(cfg, rope), _layout(layout), kind, B, max_pages,
-            _ptr(ctx_len, i32, "ctx_len", (B,)), _ptr(block_table, i32, "block_table"),
-            _ptr(q, q.dtype, "q", rows), _opt(k_self, q.dtype, "k_self", rows),
-            _opt(v_self, q.dtype, "v_self", rows), _opt(q_pos, i32, "q_pos", (B,)),
-            _ptr(out, q.dtype, "out", rows), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream()))
+    tp, tn = _table(cfg, rope, dev)
+    _call(lib.lla_q8_decode_attn, dev, cfg.ref, cache.ref(cfg, dev), tp, tn, _layout(layout), kind,
+          B, max_pages, _dense(ctx_len, _I32, dev, "ctx_len", (B,)),
+          _dense(block_table, _I32, dev, "block_table"), _dense(q, dtype, dev, "q", rows),
+          None if k_self is None else _dense(k_self, dtype, dev, "k_self", rows),
+          None if v_self is None else _dense(v_self, dtype, dev, "v_self", rows),
+          None if q_pos is None else _dense(q_pos, _I32, dev, "q_pos", (B,)),
+          _dense(out, dtype, dev, "out", rows), _dense(ws, torch.uint8, dev, "ws"), ws.numel())
     return out

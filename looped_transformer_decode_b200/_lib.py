@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from functools import cached_property
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblla.so")
@@ -59,6 +60,14 @@ class Cfg:
     def c(self) -> CCfg:
         return CCfg(self.T, self.H, self.d_head, self.r_k, self.r_v, self.mode, self.rope_base,
                     self.sm_scale, self.d_rope)
+
+    @cached_property
+    def ref(self):
+        """ctypes reference to the configuration's C struct (made once; the fields are frozen)."""
+        return ctypes.byref(self.c())
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "ref"}
 
 
 class CRopeScaling(ctypes.Structure):

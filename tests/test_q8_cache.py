@@ -67,6 +67,20 @@ def test_reference_attention_plain_loop():
 
 # ----------------------------------------------------------------------------- refusals
 
+def test_configuration_copies_after_use():
+    """The cached C struct of a configuration stays out of copies and comparisons."""
+    import copy
+    import dataclasses
+    import pickle
+    cfg = cfg_of(2, 64)
+    assert lla.q8_decode_launches(cfg, 1, 64) == 1               # makes the struct
+    for other in (pickle.loads(pickle.dumps(cfg)), copy.deepcopy(cfg), copy.copy(cfg),
+                  dataclasses.replace(cfg)):
+        assert other == cfg and hash(other) == hash(cfg)
+        assert lla.q8_decode_launches(other, 1, 64) == 1
+    assert lla.q8_decode_launches(dataclasses.replace(cfg, d_head=80), 1, 64) == -1
+
+
 PTR = ctypes.c_void_p(0x10000)
 ODD = ctypes.c_void_p(0x10008)
 BAD, NO = lla.ERR_INVALID, lla.ERR_UNSUPPORTED
