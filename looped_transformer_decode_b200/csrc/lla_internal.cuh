@@ -205,7 +205,8 @@ struct PageMapArgs {
 };
 cudaError_t launch_page_map(PageMapArgs a, cudaStream_t s);
 
-// Paged 8-bit cache (lla_q8.cu).
+// Paged 8-bit cache (lla_q8.cu; its decode attention: lla_q8_decode.cu).
+constexpr float kQ8Tiny = 1e-30f;    // a largest value at or below this counts as zero
 struct Q8AppendArgs {
   const float2* rope;              // null: keys come rotated
   int rope_max_pos, layout, d, rd, H, bf16;

@@ -1,0 +1,843 @@
+// Decode attention over the paged 8-bit cache (its layout and scales: lla_q8.cu).
+//
+// q8_decode_kernel<T, D>: HBM-bound (2 D bytes per token and head against 4 D
+// operations), so the codes never become floats one by one:
+//   scores   q is split once per item into three 7-bit integers, q = qs (q1 2^14 + q2 2^7
+//            + q3), and the dot products of four codes are one instruction each, exact in
+//            int32 (dp4a); the page's scale multiplies the finished score.
+//   values   a token's weight times its page's value scale, relative to the largest so
+//            far, is a 24-bit integer; its three bytes, of four tokens each, meet the codes
+//            of four tokens and one dim in dp4a, exact in int32 until a new largest weight
+//            rescales the sum in fp32.
+// About 1.5 instructions per code instead of the five of convert-and-multiply.
+//
+// Work: the tokens of all (sequence, head) items, in tiles of 4 KB of keys, divided among
+// the blocks from the lengths on the device, so that uneven sequences and few long ones
+// load every SM alike (see "the block's range").  Warps take a block's tiles in turn, each
+// with a ring of its own filled by bulk copies, so no warp waits for another inside an
+// item.  Pieces of one item leave partials; the last block to bring one merges them in
+// order.
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+
+#include "lla_internal.cuh"
+#include "lla_rows.cuh"
+#include "lla_sm100.cuh"
+
+namespace lla {
+namespace {
+
+constexpr int kQ8Warps = 4;
+constexpr int kQ8Threads = 32 * kQ8Warps;
+constexpr int kQ8BlocksPerSm = 3;
+constexpr int kQ8Stages = 2;
+constexpr int kQ8MinTiles = 4;              // tiles worth a block
+constexpr int kQ8ItemBlock = 12;            // start and merge of an item in tiles, for a block
+constexpr int kQ8ItemWarp = 4;              // and for a warp that has it to itself
+constexpr int kQ8FlushTiles = 4096;         // 2 * 4 * 255 * 128 per tile and dim stays below 2^31
+constexpr float kQ8Weight = 16777200.f;     // below 2^24 - 1 by more than a product's roundings
+constexpr float kQ8SmallRef = 1e-31f;       // least reference of the weights
+
+template <int D>
+struct Q8Shape {
+  // A row's lanes hold 16 of its codes each (12 of 96); a warp's load covers kRows rows, and
+  // four of them are a group, the unit of the arithmetic.  kSubs 16-token blocks, each in
+  // one page, make a group; two groups make a tile.
+  static constexpr int kLanes = D == 96 ? 8 : D / 16;
+  static constexpr int kWords = D / kLanes / 4;             // 4-code words per lane and row
+  static constexpr int kRows = 32 / kLanes;
+  static constexpr int kGroup = 4 * kRows;
+  static constexpr int kSubs = kGroup / 16;
+  static constexpr int kScores = kGroup > 32 ? 2 : 1;       // scores per lane
+  static constexpr int kParts = 2 * kSubs;                  // 16-token blocks of a tile
+  static constexpr int kTile = 16 * kParts;                 // tokens per tile
+  static constexpr int kPartBytes = 16 * D;
+  static constexpr int kHalf = kParts * kPartBytes;         // keys of a stage, then its values
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kRing = kQ8Stages * kStage;
+  // shared memory: rings, warp partials, rotated q, barriers
+  static constexpr int kPartOff = kQ8Warps * kRing;
+  static constexpr int kQOff = kPartOff + kQ8Warps * (D + 4) * 4;
+  static constexpr int kBarOff = kQOff + kQ8Warps * D * 4;
+  static constexpr int kBytes = kBarOff + kQ8Warps * kQ8Stages * 8;
+};
+
+// 2^x of x <= 0: results below 2^-126 are zero, others within two units in the last place.
+__device__ __forceinline__ float exp2_down(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// sum of four products, unsigned bytes of a with signed bytes of b
+__device__ __forceinline__ int dp4a_us(uint32_t a, uint32_t b, int c) {
+  int d;
+  asm("dp4a.u32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(const unsigned char* p, uint32_t* w) {
+  if constexpr (W == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x;
+    w[1] = u.y;
+    w[2] = u.z;
+    w[3] = u.w;
+  } else if constexpr (W == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x;
+    w[1] = u.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+}
+
+// Length of sequence b, clamped into its block table.
+__device__ __forceinline__ int q8_length(const Q8DecodeArgs& a, int b, bool tell) {
+  const long long cap = (long long)a.max_pages << a.shift;
+  const int n = a.ctx_len[b];
+  if (n >= 0 && n <= cap) return n;
+  if (tell) atomicOr(a.status, LLA_STATUS_CTX_RANGE);
+  return n < 0 ? 0 : (int)cap;
+}
+
+// What a block (or a warp) works on: tiles [t0, t1) of an item, sequence b's head h.
+struct Q8Item {
+  int b, h, n, t0, t1;
+  int c0, pieces;       // first block with a piece of the item, and how many there are
+  int slot, first_slot; // partial slot (of two per block) of this block's and of c0's piece
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q8DecodeArgs a) {
+  using S = Q8Shape<D>;
+  constexpr int W = S::kWords;
+  extern __shared__ __align__(128) unsigned char sm[];
+  float* parts = reinterpret_cast<float*>(sm + S::kPartOff);      // [warps][4 + D]
+  __shared__ uint32_t sums[kQ8Warps];
+  __shared__ int longest[kQ8Warps];
+  __shared__ unsigned long long sums3[kQ8Warps];
+  __shared__ uint32_t start_at[kQ8Warps];   // units (aligned: pieces) before the sequence
+  __shared__ int start_b[kQ8Warps];         // of a block's, or warp's, first item
+  __shared__ int abort_word, is_last, told;
+  volatile int* abort_flag = &abort_word;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  unsigned char* ring = sm + warp * S::kRing;
+  float* qs = reinterpret_cast<float*>(sm + S::kQOff) + warp * D;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kBarOff) + warp * kQ8Stages;
+
+  // ---------------------------------------------------------------- the block's range
+  // Units: an item's tiles (one for an empty item) after kQ8ItemBlock or kQ8ItemWarp more
+  // for its start and merge; the host keeps their number below 2^31.  Three ways to divide
+  // them:
+  //   aligned   the grid can give every item blocks of its own: each block gets one piece of
+  //             one item, of up to q tiles, for the least q of three that fits the grid
+  //   ranges    block c gets units [c q, c q + q): the end of one item, whole ones and a
+  //             beginning
+  //   by warp   many short items: each warp gets the items that begin in its range, whole,
+  //             and meets no other warp
+  // The one whose busiest warp has least to do is taken.
+  const int per = (a.B + kQ8Threads - 1) / kQ8Threads;
+  const int seg0 = min(tid * per, a.B), seg1 = min(seg0 + per, a.B);
+  auto tiles_of = [&](int n) { return max(1, (int)(((uint32_t)n + S::kTile - 1) / S::kTile)); };
+  uint32_t mine = 0;
+  int most = 0;
+  for (int b = seg0; b < seg1; ++b) {
+    const int tiles = tiles_of(q8_length(a, b, c == 0));
+    mine += tiles;
+    most = max(most, tiles);
+  }
+  if (tid == 0) {
+    abort_word = 0;
+    told = 0;
+  }
+  if (lane == 0) {
+    for (int s = 0; s < kQ8Stages; ++s) sm100::mbar_init(&bars[s], 1);
+    sm100::fence_mbar_init();
+  }
+  uint32_t before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    sums[warp] = before;
+    longest[warp] = most;
+  }
+  before -= mine;
+  __syncthreads();
+  uint32_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kQ8Warps; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+    most = max(most, longest[w]);
+  }
+  const uint32_t H = a.H, items = a.B * H, grid = gridDim.x, warps = grid * kQ8Warps;
+  const uint32_t block_units = (total + a.B * kQ8ItemBlock) * H;
+  const uint32_t warp_units = (total + a.B * kQ8ItemWarp) * H;
+  const uint32_t in_turn = (items + warps - 1) / warps;          // items of one warp
+  const uint32_t warp_cost = min(in_turn * (most + kQ8ItemWarp), warp_units / warps + most);
+  uint32_t block_cost = block_units / warps + kQ8ItemBlock / 2;
+  uint32_t q = 0, blocks = 0, start_pieces = 0, mine_pieces = 0;
+  bool aligned = false;
+  if (items <= grid) {
+    // pieces for three q, in fields of 21 bits: at most 444 sequences of 445 pieces
+    const uint32_t q0 = max((uint32_t)kQ8MinTiles, (total * H + grid - 1) / grid);
+    unsigned long long v = 0;
+    for (int b = seg0; b < seg1; ++b) {
+      const uint32_t tiles = tiles_of(q8_length(a, b, false));
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const uint32_t qj = q0 + j * kQ8ItemBlock / 2;
+        v += (unsigned long long)min((tiles + qj - 1) / qj, grid + 1) << (21 * j);
+      }
+    }
+    unsigned long long upto = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) sums3[warp] = upto;
+    __syncthreads();
+    unsigned long long all = 0;
+    upto -= v;
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) {
+      if (w < warp) upto += sums3[w];
+      all += sums3[w];
+    }
+#pragma unroll
+    for (int j = 2; j >= 0; --j) {
+      constexpr uint32_t kField = (1u << 21) - 1;
+      const uint32_t n = (uint32_t)(all >> (21 * j)) & kField;
+      if (n * H <= grid) {
+        aligned = true;
+        q = q0 + j * kQ8ItemBlock / 2;
+        blocks = n * H;
+        start_pieces = (uint32_t)(upto >> (21 * j)) & kField;
+        mine_pieces = (uint32_t)(v >> (21 * j)) & kField;
+      }
+    }
+    if (aligned) block_cost = min(q, (uint32_t)most) / kQ8Warps + kQ8ItemBlock / 4;
+  }
+  const bool by_warp = warp_cost < block_cost;
+  const uint32_t units = by_warp ? warp_units : block_units;
+  if (by_warp) {
+    aligned = false;
+    q = (units + warps - 1) / warps;
+    blocks = (units + kQ8Warps * q - 1) / (kQ8Warps * q);
+  } else if (!aligned) {
+    q = max((uint32_t)kQ8MinTiles, (units + grid - 1) / grid);
+    blocks = (units + q - 1) / q;
+  }
+  if (c >= blocks) return;
+  const uint32_t extra = by_warp ? kQ8ItemWarp : kQ8ItemBlock;   // an item's units before its tiles
+  const int team = by_warp ? c * kQ8Warps + warp : c;
+  const int step = by_warp ? 1 : kQ8Warps, lead = by_warp ? 0 : warp;   // a warp's tiles
+  {
+    // the sequence that the block's (or each warp's) first unit lies in
+    const int teams = by_warp ? kQ8Warps : 1;
+    const uint32_t at0 = (aligned ? start_pieces : before + seg0 * extra) * H;
+    const uint32_t end0 = at0 + (aligned ? mine_pieces : mine + (seg1 - seg0) * extra) * H;
+    for (int w = 0; w < teams; ++w) {
+      const uint32_t x = aligned ? c : (c * teams + w) * q;
+      if (x < at0 || x >= end0) continue;
+      uint32_t at = at0;
+      int b = seg0;
+      for (; b < seg1 - 1; ++b) {
+        const uint32_t tiles = tiles_of(q8_length(a, b, false));
+        const uint32_t len = (aligned ? (tiles + q - 1) / q : tiles + extra) * H;
+        if (x < at + len) break;
+        at += len;
+      }
+      start_b[w] = b;
+      start_at[w] = at;
+    }
+  }
+  __syncthreads();
+
+  // ---------------------------------------------------------------- its items
+  const int r = lane / S::kLanes, col = lane % S::kLanes;      // row of a load, its dims
+  uint32_t used = 0;                                // tiles this warp has put through its ring
+  bool aborted = false;
+  uint32_t u = team * q;                            // next unit
+  const uint32_t u1 = min(u + q, units);
+  const int at_w = by_warp ? warp : 0;
+  uint32_t seq_at = start_at[at_w];                 // first unit (piece) of sequence it.b
+  Q8Item it;
+  it.b = start_b[at_w];
+  // the item that unit u lies in, or the block's piece (aligned); false: there is none
+  auto find_item = [&]() {
+    if (aligned) {
+      it.n = q8_length(a, it.b, false);
+      const uint32_t tiles = tiles_of(it.n), pieces = (tiles + q - 1) / q, k = c - seq_at;
+      it.h = k / pieces;
+      const uint32_t part = k - it.h * pieces, base = tiles / pieces, rem = tiles - base * pieces;
+      it.t0 = part * base + min(part, rem);
+      it.t1 = it.t0 + base + (part < rem ? 1 : 0);
+      it.c0 = c - part;
+      it.pieces = pieces;
+      it.slot = it.first_slot = 0;
+      return true;
+    }
+    while (u < u1) {
+      uint32_t len;
+      for (;;) {
+        it.n = q8_length(a, it.b, false);
+        len = tiles_of(it.n) + extra;
+        if (u < seq_at + len * H) break;
+        seq_at += len * H;
+        ++it.b;
+      }
+      it.h = (u - seq_at) / len;
+      const uint32_t item0 = seq_at + it.h * len, tile0 = item0 + extra;
+      if (by_warp) {
+        const bool begun = u > item0;               // in the range before this one
+        u = item0 + len;
+        if (begun) continue;
+        it.t0 = 0;
+        it.t1 = len - extra;
+        it.pieces = 1;
+        return true;
+      }
+      const uint32_t end = min(item0 + len, u1);
+      it.t0 = u > tile0 ? u - tile0 : 0;
+      it.t1 = end > tile0 ? end - tile0 : 0;
+      u = end;
+      if (it.t0 == it.t1) continue;                 // its tiles are all in the next range
+      it.c0 = tile0 / q;
+      it.pieces = (item0 + len - 1) / q - it.c0 + 1;
+      // slot 0: the first item of a block's range, slot 1: a later one, which is its last
+      it.slot = item0 <= c * q ? 0 : 1;
+      it.first_slot = item0 <= it.c0 * q ? 0 : 1;
+      return true;
+    }
+    return false;
+  };
+
+  // Lane g < kParts looks after block g of each tile: its page id (loaded two tiles ahead of
+  // the tile's use), its copies, its scales (loaded one tile ahead).
+  const size_t page_step = (size_t)a.H << a.shift;             // rows per page, all heads
+  bool bad = false;
+  auto part_id = [&](int t) {
+    if (lane >= S::kParts || t >= it.t1) return -1;
+    const int tok = t * S::kTile + lane * 16;                  // lengths stay below 2^31
+    return tok < it.n ? __ldg(a.block_table + (long long)it.b * a.max_pages + (tok >> a.shift)) : -1;
+  };
+  auto checked = [&](int t, int id) {                          // -1 for what is not there
+    const bool there = lane < S::kParts && t < it.t1 && t * S::kTile + lane * 16 < it.n;
+    const bool ok = there && id >= 0 && id < a.n_pages;
+    bad |= there && !ok;
+    return ok ? id : -1;
+  };
+  auto issue = [&](int t, int id, uint32_t seq) {              // tile t, the warp's seq-th
+    if (t >= it.t1) return;
+    const int s = seq % kQ8Stages;
+    const unsigned live = __ballot_sync(0xffffffffu, id >= 0);
+    if (lane == 0) sm100::mbar_arrive_expect_tx(&bars[s], __popc(live) * 2 * S::kPartBytes);
+    __syncwarp();
+    if (id >= 0) {
+      const int tok = t * S::kTile + lane * 16;
+      const size_t run = (id * page_step + ((size_t)it.h << a.shift) +
+                          (tok & ((1 << a.shift) - 1))) * D;
+      unsigned char* st = ring + s * S::kStage + lane * S::kPartBytes;
+      sm100::bulk_load(st, a.kc + run, S::kPartBytes, &bars[s]);
+      sm100::bulk_load(st + S::kHalf, a.vc + run, S::kPartBytes, &bars[s]);
+    }
+  };
+  auto scale_of = [&](const float* scales, int id) {
+    return id >= 0 ? __ldg(scales + (size_t)id * a.H + it.h) : 0.f;
+  };
+  int id0 = -1, id1 = -1, id2 = -1;                            // a warp's next three tiles
+  float ks0 = 0.f, vs0 = 0.f;
+  auto load_ids = [&]() {
+    const int first = it.t0 + lead;
+    id0 = part_id(first);
+    id1 = part_id(first + step);
+    id2 = part_id(first + 2 * step);
+  };
+  auto start_copies = [&]() {
+    const int first = it.t0 + lead;
+    id0 = checked(first, id0);
+    id1 = checked(first + step, id1);
+    if (!aborted) {
+      issue(first, id0, used);
+      issue(first + step, id1, used + 1);
+    }
+    ks0 = scale_of(a.ks, id0);
+    vs0 = scale_of(a.vs, id0);
+  };
+  bool more = find_item(), started = false;
+  unsigned finished = 0;                                       // blocks that finished before
+  auto finish_block = [&]() {
+    if (told || c == 0) __threadfence();                       // block 0 tells of lengths
+    return atomicAdd(a.counter, 1u);
+  };
+  if (more) load_ids();
+  while (more) {
+    const int first = it.t0 + lead;
+    const size_t bh = (size_t)it.b * a.H + it.h;
+
+    // q rotated at q_pos, through shared memory, by each warp for itself; the in-flight
+    // token's score, which needs no rotation, both sitting at q_pos
+    float self = 0.f;
+    {
+      const bool turn = a.rope != nullptr;
+      const RowChunk rc = row_chunk(lane, D, a.rd, turn ? a.layout : LLA_ROPE_INTERLEAVED);
+      float v[8], k[8];
+      int asked = 0;
+      if (lane < D / 8) {
+        if (turn) asked = a.q_pos[it.b];
+        load_chunk(static_cast<const T*>(a.q) + bh * D, rc, v);
+        if (a.k_self) load_chunk(static_cast<const T*>(a.k_self) + bh * D, rc, k);
+      }
+      if (!started) start_copies();
+      started = true;
+      if (lane < D / 8) {
+        if (a.k_self) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) self = fmaf(v[j], k[j], self);
+        }
+        if (turn) {
+          const int pos = checked_position(asked, a.rope_max_pos, nullptr, false);
+          if (lane == 0 && pos != asked) {
+            atomicOr(a.status, LLA_STATUS_POSITION_RANGE);
+            told = 1;
+          }
+          rotate_chunk(a.rope + (size_t)pos * (a.rd / 2), rc, 1.f, v);
+        }
+        store4(qs + rc.lo, v);
+        store4(qs + rc.hi, v + 4);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) self += __shfl_xor_sync(0xffffffffu, self, off);
+    self *= a.kappa;
+    __syncwarp();
+
+    // q as three signed digits of 7 bits, the largest |q| at 127 * 2^14: a lane splits four
+    // dims and takes the words of its own through shared memory
+    uint32_t q1[W], q2[W], q3[W];
+    float score_scale;
+    bool strange = false;                                       // a NaN or an infinity in q
+    {
+      float v[4] = {0.f, 0.f, 0.f, 0.f}, amax = 0.f;
+      if (lane < D / 4) load4(qs + 4 * lane, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        amax = fmaxf(amax, fabsf(v[j]));
+        strange |= !(fabsf(v[j]) <= FLT_MAX);
+      }
+      strange = __any_sync(0xffffffffu, strange);               // and the values are read
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      constexpr float kTop = 127.f * 16384.f;
+      const float inv = amax > kQ8Tiny ? kTop / amax : 0.f;
+      score_scale = strange ? 0.f : a.kappa * amax / kTop;      // strange: pl becomes NaN below
+      uint32_t hi = 0, mid = 0, lo = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int x = __float2int_rn(v[j] * inv), y = (x + 64) >> 7, z = (y + 64) >> 7;
+        lo |= (uint32_t)((x - (y << 7)) & 255) << (8 * j);      // -64 .. 63
+        mid |= (uint32_t)((y - (z << 7)) & 255) << (8 * j);
+        hi |= (uint32_t)(z & 255) << (8 * j);                   // -127 .. 127
+      }
+      uint32_t* words = reinterpret_cast<uint32_t*>(qs);
+      if (lane < D / 4) {
+        words[lane] = hi;
+        words[D / 4 + lane] = mid;
+        words[D / 2 + lane] = lo;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        q1[w] = words[col * W + w];
+        q2[w] = words[D / 4 + col * W + w];
+        q3[w] = words[D / 2 + col * W + w];
+      }
+    }
+
+    // Sums are relative to 2^m, m the largest score so far: l of 2^(s - m), o of
+    // 2^(s - m) v.  acc holds weights w = 2^(s - m) vs / R * kQ8Weight times codes, R
+    // the reference that no weight since the last flush exceeds.  A larger weight flushes
+    // acc into o; a larger score rescales l, o and R.
+    float m = -INFINITY, l = 0.f, R = 0.f, wf = 0.f;             // wf = kQ8Weight / R
+    float o[4 * W];
+    int acc1[4 * W], acc2[4 * W], acc3[4 * W];
+#pragma unroll
+    for (int j = 0; j < 4 * W; ++j) {
+      o[j] = 0.f;
+      acc1[j] = acc2[j] = acc3[j] = 0;
+    }
+    int since = 0;                                               // tiles since the last flush
+    bool held = false;                                           // acc holds something
+    auto flush = [&]() {
+      if (!held) return;
+      held = false;
+      const float f = R * (1.f / kQ8Weight);
+#pragma unroll
+      for (int j = 0; j < 4 * W; ++j) {
+        o[j] = fmaf(f, fmaf((float)acc1[j], 65536.f, fmaf((float)acc2[j], 256.f, (float)acc3[j])),
+                    o[j]);
+        acc1[j] = acc2[j] = acc3[j] = 0;
+      }
+      since = 0;
+    };
+
+    // Rows r + kRows i of a group are a lane's, i = 0 .. 3; it ends up with the scores of
+    // i_own (and i_own + 1 when it has two).
+    const int i_own = S::kLanes == 8 ? (((col >> 1) & 1) | ((col >> 1) & 2))
+                                     : S::kLanes == 4 ? (((col & 1)) | (col & 2)) : 2 * col;
+    uint32_t seq = used;
+    for (int t = first; t < it.t1 && !aborted; t += step, ++seq) {
+      const int s = seq % kQ8Stages;
+      const unsigned live = __ballot_sync(0xffffffffu, id0 >= 0);
+      // scales of the next tile, page ids of the one after it
+      const float ks1 = scale_of(a.ks, id1), vs1 = scale_of(a.vs, id1);
+      id2 = checked(t + 2 * step, id2);
+      const int id3 = part_id(t + 3 * step);
+      if (!sm100::mbar_wait(&bars[s], (seq / kQ8Stages) & 1u, abort_flag)) {
+        // copies already issued land before the block can end
+        for (int k = 0; k < kQ8Stages && t + k * step < it.t1; ++k) {
+          const unsigned long long w0 = sm100::global_timer_ns();
+          while (!sm100::mbar_try_wait(&bars[(seq + k) % kQ8Stages], ((seq + k) / kQ8Stages) & 1u) &&
+                 sm100::global_timer_ns() - w0 < sm100::kWaitTimeoutNs) {
+          }
+        }
+        aborted = true;
+        break;
+      }
+      if (++since >= kQ8FlushTiles) flush();
+      const unsigned char* st = ring + s * S::kStage + r * D + col * 4 * W;
+      const int rows_left = it.n - t * S::kTile - r - S::kRows * i_own;   // of a lane's first score
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (!(live >> (g * S::kSubs) & ((1 << S::kSubs) - 1))) continue;  // warp-uniform
+        const unsigned char* kp = st + g * S::kSubs * S::kPartBytes;
+        float part[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t kw[W];
+          load_words<W>(kp + i * S::kRows * D, kw);
+          int s1 = 0, s2 = 0, s3 = 0;
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            s1 = __dp4a((int)kw[w], (int)q1[w], s1);
+            s2 = __dp4a((int)kw[w], (int)q2[w], s2);
+            s3 = __dp4a((int)kw[w], (int)q3[w], s3);
+          }
+          part[i] = fmaf((float)(s1 * 128 + s2), 128.f, (float)s3);
+        }
+        // sums over a row's lanes, each exchange halving what a lane holds
+        constexpr int kFar = S::kLanes / 2, kNear = S::kLanes / 4;
+        const bool upper = col & kFar;
+        float x[2];
+        x[0] = (upper ? part[2] : part[0]) +
+               __shfl_xor_sync(0xffffffffu, upper ? part[0] : part[2], kFar);
+        x[1] = (upper ? part[3] : part[1]) +
+               __shfl_xor_sync(0xffffffffu, upper ? part[1] : part[3], kFar);
+        if constexpr (S::kLanes >= 4) {
+          const bool odd = col & kNear;
+          x[0] = (odd ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], kNear);
+        }
+        if constexpr (S::kLanes == 8) x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+        float sc[S::kScores], vsc[S::kScores];
+        bool above = false, heavy = false;
+#pragma unroll
+        for (int k = 0; k < S::kScores; ++k) {
+          // the 16-token block of the group that the row lies in
+          const int sub = g * S::kSubs + (S::kSubs == 1 ? 0 : S::kSubs == 2 ? i_own >> 1 : i_own + k);
+          const float ksc = __shfl_sync(0xffffffffu, ks0, sub) * score_scale;
+          vsc[k] = __shfl_sync(0xffffffffu, vs0, sub);
+          const bool there = rows_left > g * S::kGroup + k * S::kRows && (live >> sub & 1);
+          sc[k] = there ? x[k] * ksc : -INFINITY;
+          above |= sc[k] > m;
+          heavy |= vsc[k] > R;                                  // weights are at most vs: p <= 1
+        }
+        if (__any_sync(0xffffffffu, above)) {
+          float mt = S::kScores == 2 ? fmaxf(sc[0], sc[S::kScores - 1]) : sc[0];
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1)
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+          const float f = exp2_down(m - mt);                    // 0 the first time
+          m = mt;
+          l *= f;
+          R *= f;
+#pragma unroll
+          for (int j = 0; j < 4 * W; ++j) o[j] *= f;
+          if (R < kQ8SmallRef) {                                // 1 / R stays finite
+            flush();
+            R = kQ8SmallRef;
+          }
+          wf = kQ8Weight / R;
+          heavy = true;
+        }
+        if (__any_sync(0xffffffffu, heavy)) {
+          float top = S::kScores == 2 ? fmaxf(vsc[0], vsc[S::kScores - 1]) : vsc[0];
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          if (top > R) {
+            flush();
+            R = top;
+            wf = kQ8Weight / R;
+          }
+        }
+        uint32_t wt[S::kScores];
+#pragma unroll
+        for (int k = 0; k < S::kScores; ++k) {
+          const float p = exp2_down(sc[k] - m);
+          l += p;
+          wt[k] = __float2uint_rn(p * (vsc[k] * wf));
+        }
+        // the weights of a lane's four rows, then their bytes: hi, mid, lo words of four tokens
+        uint32_t e0 = wt[0], e1 = wt[S::kScores - 1];
+        if constexpr (S::kLanes >= 4) {
+          const uint32_t other = __shfl_xor_sync(0xffffffffu, wt[0], kNear);
+          const bool odd = col & kNear;
+          e0 = odd ? other : wt[0];
+          e1 = odd ? wt[0] : other;
+        }
+        const uint32_t f0 = __shfl_xor_sync(0xffffffffu, e0, kFar);
+        const uint32_t f1 = __shfl_xor_sync(0xffffffffu, e1, kFar);
+        const uint32_t g0 = upper ? f0 : e0, g1 = upper ? f1 : e1;
+        const uint32_t g2 = upper ? e0 : f0, g3 = upper ? e1 : f1;
+        const uint32_t a01 = __byte_perm(g0, g1, 0x5140), a23 = __byte_perm(g2, g3, 0x5140);
+        const uint32_t h01 = __byte_perm(g0, g1, 0x0062), h23 = __byte_perm(g2, g3, 0x0062);
+        const uint32_t wlo = __byte_perm(a01, a23, 0x5410), wmid = __byte_perm(a01, a23, 0x7632);
+        const uint32_t whi = __byte_perm(h01, h23, 0x5410);
+        held = true;
+        uint32_t vw[4][W];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_words<W>(kp + S::kHalf + i * S::kRows * D, vw[i]);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          // four rows of four dims, turned into four dims of four rows
+          const uint32_t y0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
+          const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
+          const uint32_t y2 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+          const uint32_t y3 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+          const uint32_t dim[4] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632),
+                                   __byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc1[4 * w + j] = dp4a_us(whi, dim[j], acc1[4 * w + j]);
+            acc2[4 * w + j] = dp4a_us(wmid, dim[j], acc2[4 * w + j]);
+            acc3[4 * w + j] = dp4a_us(wlo, dim[j], acc3[4 * w + j]);
+          }
+        }
+      }
+      __syncwarp();                                             // the stage is read
+      issue(t + kQ8Stages * step, id2, seq + kQ8Stages);
+      id0 = id1;
+      id1 = id2;
+      id2 = id3;
+      ks0 = ks1;
+      vs0 = vs1;
+    }
+    if (it.t1 > first) used += (it.t1 - first + step - 1) / step;
+    if (__any_sync(0xffffffffu, bad) && lane == 0) {
+      atomicOr(a.status, LLA_STATUS_PAGE_RANGE);
+      told = 1;
+    }
+    bad = false;
+    if (aborted && lane == 0) {
+      atomicOr(a.status, LLA_STATUS_TIMEOUT);
+      told = 1;
+    }
+    // the next item's first tiles are on their way while this one is merged
+    const Q8Item now = it;
+    more = !aligned && find_item();
+    if (more) {
+      load_ids();
+      start_copies();
+    }
+
+    // ---------------------------------------------------------------- merge the warps
+    flush();
+    if (S::kLanes == 8) l *= 0.5f;                              // two lanes held every score
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, off);
+      if (off < S::kLanes) continue;
+#pragma unroll
+      for (int j = 0; j < 4 * W; ++j) o[j] += __shfl_xor_sync(0xffffffffu, o[j], off);
+    }
+    if (by_warp) {
+      float f = 1.f, fs = 0.f;
+      if (a.k_self) {
+        const float top = fmaxf(m, self);
+        f = m > -INFINITY ? exp2f(m - top) : 0.f;
+        fs = exp2f(self - top);
+      }
+      l = fmaf(l, f, fs);
+      if (strange && l != 0.f) l = NAN;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (r == 0) {
+        const size_t at = bh * D + col * 4 * W;
+#pragma unroll
+        for (int j = 0; j < 4 * W; j += 4) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          if (a.k_self) load4(static_cast<const T*>(a.v_self) + at + j, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            v[i] = l == 0.f ? 0.f : (a.k_self ? fmaf(o[j + i], f, fs * v[i]) : o[j + i]) * inv;
+          store4(static_cast<T*>(a.out) + at + j, v);
+        }
+      }
+      continue;
+    }
+    float v_own = 0.f;
+    if (a.k_self && tid < D) v_own = as_float(static_cast<const T*>(a.v_self)[bh * D + tid]);
+    float* pw = parts + warp * (D + 4);
+    if (r == 0) {
+#pragma unroll
+      for (int j = 0; j < 4 * W; ++j) pw[4 + col * 4 * W + j] = o[j];
+      if (lane == 0) {
+        pw[0] = m;
+        pw[1] = l;
+      }
+    }
+    __syncthreads();
+    // every status bit of the block is told; the count comes back during the merge
+    if (tid == 0 && !more) finished = finish_block();
+    float pm = -INFINITY, pl = 0.f, po = 0.f;
+#pragma unroll
+    for (int w = 0; w < kQ8Warps; ++w) pm = fmaxf(pm, parts[w * (D + 4)]);
+    if (pm > -INFINITY) {
+#pragma unroll
+      for (int w = 0; w < kQ8Warps; ++w) {
+        const float f = exp2f(parts[w * (D + 4)] - pm);
+        pl = fmaf(parts[w * (D + 4) + 1], f, pl);
+        if (tid < D) po = fmaf(parts[w * (D + 4) + 4 + tid], f, po);
+      }
+    }
+
+    // ---------------------------------------------------------------- the item's other blocks
+    bool finish = true;
+    if (now.pieces > 1) {
+      float* mine_p = a.partials + (size_t)(2 * c + now.slot) * (D + 2);
+      if (tid < D) __stcg(mine_p + 2 + tid, po);
+      if (tid == 0) {
+        __stcg(mine_p, pm);
+        __stcg(mine_p + 1, pl);
+      }
+      __syncthreads();
+      if (tid == 0) {
+        __threadfence();
+        const unsigned got = atomicAdd(a.piece_counters + now.c0, 1u);
+        is_last = got == (unsigned)now.pieces - 1;
+        if (is_last) a.piece_counters[now.c0] = 0;
+        __threadfence();
+      }
+      __syncthreads();
+      finish = is_last;
+      if (finish) {
+        // in the order of the pieces, four at a time
+        pm = -INFINITY;
+        pl = po = 0.f;
+        for (int k0 = 0; k0 < now.pieces; k0 += 4) {
+          float mm[4], ll[4], oo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = k0 + k;
+            const float* pp = a.partials +
+                (size_t)(2 * (now.c0 + i) + (i == 0 ? now.first_slot : 0)) * (D + 2);
+            mm[k] = i < now.pieces ? __ldcg(pp) : -INFINITY;
+            ll[k] = i < now.pieces ? __ldcg(pp + 1) : 0.f;
+            oo[k] = i < now.pieces && tid < D ? __ldcg(pp + 2 + tid) : 0.f;
+          }
+          const float top = fmaxf(fmaxf(fmaxf(mm[0], mm[1]), fmaxf(mm[2], mm[3])), pm);
+          if (!(top > -INFINITY)) continue;
+          const float f0 = exp2f(pm - top);
+          pl *= f0;
+          po *= f0;
+          pm = top;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float f = exp2f(mm[k] - top);
+            pl = fmaf(ll[k], f, pl);
+            po = fmaf(oo[k], f, po);
+          }
+        }
+      }
+    }
+    if (finish) {
+      if (a.k_self) {
+        const float top = fmaxf(pm, self);
+        const float f = pm > -INFINITY ? exp2f(pm - top) : 0.f, fs = exp2f(self - top);
+        pl = fmaf(pl, f, fs);
+        po = fmaf(po, f, fs * v_own);
+      }
+      if (strange && pl != 0.f) pl = NAN;
+      if (tid < D) put(static_cast<T*>(a.out) + bh * D + tid, pl == 0.f ? 0.f : po / pl);
+    }
+    __syncthreads();                                            // parts and is_last are free
+  }
+  // the last block to finish publishes the call's status word and re-arms the counter
+  if (by_warp || !started) {                                   // also a range without a tile
+    __syncthreads();
+    if (tid == 0) finished = finish_block();
+  }
+  if (tid == 0 && finished == blocks - 1) {
+    __threadfence();
+    a.status[1] = atomicExch(&a.status[0], 0);
+    atomicExch(a.counter, 0u);
+  }
+}
+
+int q8_max_blocks() { return sm_count() * kQ8BlocksPerSm; }
+
+template <typename T, int D>
+cudaError_t launch_decode_td(const Q8DecodeArgs& a, cudaStream_t s) {
+  using S = Q8Shape<D>;
+  cudaError_t e = cudaFuncSetAttribute(q8_decode_kernel<T, D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (e != cudaSuccess) return e;
+  const long long tiles =
+      (((long long)a.max_pages << a.shift) + S::kTile - 1) / S::kTile;
+  // at most one block per kQ8MinTiles tiles of every item
+  const long long per_item = std::max(1LL, (tiles + kQ8MinTiles - 1) / kQ8MinTiles);
+  const long long grid = std::min<long long>((long long)a.B * a.H * per_item, q8_max_blocks());
+  q8_decode_kernel<T, D><<<(unsigned)grid, kQ8Threads, S::kBytes, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_decode_t(const Q8DecodeArgs& a, cudaStream_t s) {
+  switch (a.d) {
+    case 32: return launch_decode_td<T, 32>(a, s);
+    case 64: return launch_decode_td<T, 64>(a, s);
+    case 96: return launch_decode_td<T, 96>(a, s);
+    case 128: return launch_decode_td<T, 128>(a, s);
+    default: return cudaErrorNotSupported;
+  }
+}
+
+}  // namespace
+
+// Workspace: header, one counter per block, two partials per block.
+size_t q8_decode_counters_at() { return kWsHeader; }
+size_t q8_decode_partials_at() { return kWsHeader + align_up((size_t)q8_max_blocks() * 4, 256); }
+size_t q8_decode_ws_bytes(const lla_cfg& c, int, int) {
+  return q8_decode_partials_at() + (size_t)q8_max_blocks() * 2 * (c.d_head + 2) * 4;
+}
+
+cudaError_t launch_q8_decode(const Q8DecodeArgs& a, cudaStream_t s) {
+  return a.bf16 ? launch_decode_t<__nv_bfloat16>(a, s) : launch_decode_t<float>(a, s);
+}
+
+}  // namespace lla
