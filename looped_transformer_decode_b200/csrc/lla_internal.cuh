@@ -177,6 +177,7 @@ cudaError_t launch_full_decode(const FullDecodeParams& p, const void* k_full, co
 struct RopeApplyArgs {
   const float2* rope;              // [rope_max_pos][rd/2]
   int rope_max_pos, d, rd, layout, n_heads, bf16;
+  int groups, tok_block;           // the launch's shape
   float sign;                      // 1, or -1 for the inverse rotation
   long long n_tok, x_stride, y_stride;   // strides between tokens, in elements
   const int32_t* positions;
@@ -211,6 +212,7 @@ struct Q8AppendArgs {
   const float2* rope;              // null: keys come rotated
   int rope_max_pos, layout, d, rd, H, bf16;
   int B, shift, max_pages, n_pages, n_tok;
+  int team, groups;                // the launch's shape for prompts
   const int32_t* ctx_len;          // lengths with the new tokens
   const int32_t* block_table;
   const int32_t* tok_start;
@@ -226,6 +228,7 @@ struct Q8AppendArgs {
 };
 struct Q8ReadArgs {
   int d, H, shift, n_pages;
+  int row_block;                   // the launch's shape
   long long n_rows;
   const int64_t* slot;
   const int8_t* kc;
@@ -258,7 +261,7 @@ struct Q8DecodeArgs {
   float* partials;                 // [blocks][2][2 + d]
 };
 cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s);
-cudaError_t launch_q8_read(const Q8ReadArgs& a, cudaStream_t s);
+cudaError_t launch_q8_read(Q8ReadArgs a, cudaStream_t s);
 size_t q8_decode_ws_bytes(const lla_cfg& c, int B, int n_cap);
 size_t q8_decode_counters_at();
 size_t q8_decode_partials_at();

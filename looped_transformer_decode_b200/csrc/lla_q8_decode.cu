@@ -396,13 +396,13 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     float self = 0.f;
     {
       const bool turn = a.rope != nullptr;
-      const RowChunk rc = row_chunk(lane, D, a.rd, turn ? a.layout : LLA_ROPE_INTERLEAVED);
+      const RowChunk rc = row_chunk<8>(lane, D, turn ? a.rd : 0, a.layout);
       float v[8], k[8];
       int asked = 0;
       if (lane < D / 8) {
         if (turn) asked = a.q_pos[it.b];
-        load_chunk(static_cast<const T*>(a.q) + bh * D, rc, v);
-        if (a.k_self) load_chunk(static_cast<const T*>(a.k_self) + bh * D, rc, k);
+        load_chunk<8>(static_cast<const T*>(a.q) + bh * D, rc, v);
+        if (a.k_self) load_chunk<8>(static_cast<const T*>(a.k_self) + bh * D, rc, k);
       }
       if (!started) start_copies();
       started = true;
@@ -417,10 +417,10 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
             atomicOr(a.status, LLA_STATUS_POSITION_RANGE);
             told = 1;
           }
-          rotate_chunk(a.rope + (size_t)pos * (a.rd / 2), rc, 1.f, v);
+          if (rc.rotary)
+            rotate_chunk<8>(load_turn<8>(a.rope + (size_t)pos * (a.rd / 2), rc), rc.split, v);
         }
-        store4(qs + rc.lo, v);
-        store4(qs + rc.hi, v + 4);
+        store_chunk<8>(qs, rc, v);
       }
     }
 #pragma unroll
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     bool strange = false;                                       // a NaN or an infinity in q
     {
       float v[4] = {0.f, 0.f, 0.f, 0.f}, amax = 0.f;
-      if (lane < D / 4) load4(qs + 4 * lane, v);
+      if (lane < D / 4) load_run<4>(qs + 4 * lane, v);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         amax = fmaxf(amax, fabsf(v[j]));
@@ -691,11 +691,11 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
 #pragma unroll
         for (int j = 0; j < 4 * W; j += 4) {
           float v[4] = {0.f, 0.f, 0.f, 0.f};
-          if (a.k_self) load4(static_cast<const T*>(a.v_self) + at + j, v);
+          if (a.k_self) load_run<4>(static_cast<const T*>(a.v_self) + at + j, v);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             v[i] = l == 0.f ? 0.f : (a.k_self ? fmaf(o[j + i], f, fs * v[i]) : o[j + i]) * inv;
-          store4(static_cast<T*>(a.out) + at + j, v);
+          store_run<4>(static_cast<T*>(a.out) + at + j, v);
         }
       }
       continue;

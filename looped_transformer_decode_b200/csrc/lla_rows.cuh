@@ -1,8 +1,9 @@
-// Rows of one head (d dims, fp32 or bf16) cut into chunks of eight dims, one thread
-// each, such that both dims of every rotary pair belong to one thread:
-//   interleaved pairs, and dims past the rotary ones   eight consecutive dims
-//   half-split pairs                                    4 c .. 4 c + 3 and rd/2 above them
-// rd and d are multiples of 32, so chunks never straddle the rotary dims' end.
+// Rows of one head (d dims, fp32 or bf16) cut into chunks of N dims (8 or 16), one thread
+// each, such that both dims of every rotary pair belong to one thread: two runs of N / 2
+// dims, half of the rotary dims apart (past them: half of the others).  Neighbouring threads
+// hold neighbouring runs, so a warp's access to its first runs, or its second, is contiguous.
+// The first run holds the first dims of half-split pairs and the second run the second ones;
+// interleaved pairs lie within a run.  rd and d are multiples of 32.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -12,83 +13,125 @@
 
 namespace lla {
 
+// Dims in two 16-byte accesses.
+template <typename T>
+constexpr int kChunkDims = 32 / (int)sizeof(T);
+
 struct RowChunk {
-  int lo, hi;    // first dim of each group of four
-  int pair;      // first rotary pair, or -1 past the rotary dims
-  bool split;    // half-split: v[j] pairs with v[j + 4]; else v[2 j] with v[2 j + 1]
+  int lo, hi;    // first dim of each run
+  bool rotary;   // else past the rotary dims
+  bool split;    // half-split pairs (v[j], v[j + N/2]); else (v[2 j], v[2 j + 1])
 };
 
+template <int N>
 __device__ __forceinline__ RowChunk row_chunk(int c, int d, int rd, int layout) {
   RowChunk r;
-  if (c * 8 >= rd) {
-    r.lo = c * 8;
-    r.hi = r.lo + 4;
-    r.pair = -1;
-    r.split = false;
-  } else if (layout == LLA_ROPE_HALF) {
-    r.lo = c * 4;
-    r.hi = rd / 2 + c * 4;
-    r.pair = c * 4;
-    r.split = true;
-  } else {
-    r.lo = c * 8;
-    r.hi = r.lo + 4;
-    r.pair = c * 4;
-    r.split = false;
-  }
+  r.rotary = c * N < rd;
+  r.split = layout == LLA_ROPE_HALF;
+  const int past = r.rotary ? 0 : rd / 2;
+  r.lo = past + c * (N / 2);
+  r.hi = r.lo + (r.rotary ? rd / 2 : (d - rd) / 2);
   return r;
 }
 
-__device__ __forceinline__ void load4(const float* p, float* v) {
-  const float4 f = *reinterpret_cast<const float4*>(p);
-  v[0] = f.x;
-  v[1] = f.y;
-  v[2] = f.z;
-  v[3] = f.w;
+// Four or eight elements to fp32 and back.
+template <int M>
+__device__ __forceinline__ void load_run(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < M; i += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(p + i);
+    v[i] = f.x;
+    v[i + 1] = f.y;
+    v[i + 2] = f.z;
+    v[i + 3] = f.w;
+  }
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* v) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(u.x << 16);
-  v[1] = __uint_as_float(u.x & 0xffff0000u);
-  v[2] = __uint_as_float(u.y << 16);
-  v[3] = __uint_as_float(u.y & 0xffff0000u);
+__device__ __forceinline__ void unpack_bf16x2(uint32_t u, float* v) {
+  v[0] = __uint_as_float(u << 16);
+  v[1] = __uint_as_float(u & 0xffff0000u);
+}
+template <int M>
+__device__ __forceinline__ void load_run(const __nv_bfloat16* p, float* v) {
+  if constexpr (M == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    unpack_bf16x2(u.x, v);
+    unpack_bf16x2(u.y, v + 2);
+    unpack_bf16x2(u.z, v + 4);
+    unpack_bf16x2(u.w, v + 6);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    unpack_bf16x2(u.x, v);
+    unpack_bf16x2(u.y, v + 2);
+  }
 }
 __device__ __forceinline__ uint32_t bf16x2_bits(float a, float b) {
   const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&t);
 }
-__device__ __forceinline__ void store4(float* p, const float* v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float* v) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
-}
-
-template <typename T>
-__device__ __forceinline__ void load_chunk(const T* row, const RowChunk& rc, float* v) {
-  load4(row + rc.lo, v);
-  load4(row + rc.hi, v + 4);
-}
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* row, const RowChunk& rc, const float* v) {
-  store4(row + rc.lo, v);
-  store4(row + rc.hi, v + 4);
-}
-
-// Rotate a chunk by the table row of its position; sign = -1 rotates back.
-__device__ __forceinline__ void rotate_chunk(const float2* table_row, const RowChunk& rc,
-                                             float sign, float* v) {
-  if (rc.pair < 0) return;
-  const float4* t = reinterpret_cast<const float4*>(table_row + rc.pair);
-  const float4 t0 = __ldg(t), t1 = __ldg(t + 1);
-  const float c[4] = {t0.x, t0.z, t1.x, t1.z};
-  const float s[4] = {sign * t0.y, sign * t0.w, sign * t1.y, sign * t1.w};
+template <int M>
+__device__ __forceinline__ void store_run(float* p, const float* v) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int ia = rc.split ? j : 2 * j, ib = rc.split ? j + 4 : 2 * j + 1;
-    const float a = v[ia], b = v[ib];
-    v[ia] = a * c[j] - b * s[j];
-    v[ib] = a * s[j] + b * c[j];
+  for (int i = 0; i < M; i += 4)
+    *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+template <int M>
+__device__ __forceinline__ void store_run(__nv_bfloat16* p, const float* v) {
+  if constexpr (M == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
+                                              bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+  else
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+}
+
+template <int N, typename T>
+__device__ __forceinline__ void load_chunk(const T* row, const RowChunk& rc, float* v) {
+  load_run<N / 2>(row + rc.lo, v);
+  load_run<N / 2>(row + rc.hi, v + N / 2);
+}
+template <int N, typename T>
+__device__ __forceinline__ void store_chunk(T* row, const RowChunk& rc, const float* v) {
+  store_run<N / 2>(row + rc.lo, v);
+  store_run<N / 2>(row + rc.hi, v + N / 2);
+}
+
+// (cos, sin) of a chunk's pairs at a position: its table row.
+template <int N>
+struct Turn {
+  float c[N / 2], s[N / 2];
+};
+template <int N>
+__device__ __forceinline__ Turn<N> load_turn(const float2* table_row, const RowChunk& rc) {
+  Turn<N> t;
+  const float4* lo = reinterpret_cast<const float4*>(table_row + (rc.split ? rc.lo : rc.lo / 2));
+  const float4* hi = rc.split ? lo + N / 8 : reinterpret_cast<const float4*>(table_row + rc.hi / 2);
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    const float4 f = i < N / 8 ? __ldg(lo + i) : __ldg(hi + i - N / 8);
+    t.c[2 * i] = f.x;
+    t.s[2 * i] = f.y;
+    t.c[2 * i + 1] = f.z;
+    t.s[2 * i + 1] = f.w;
+  }
+  return t;
+}
+
+// Rotate a chunk of a head's rotary dims.
+template <int N>
+__device__ __forceinline__ void rotate_chunk(const Turn<N>& t, bool split, float* v) {
+  if (split) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const float a = v[j], b = v[j + N / 2];
+      v[j] = a * t.c[j] - b * t.s[j];
+      v[j + N / 2] = a * t.s[j] + b * t.c[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const float a = v[2 * j], b = v[2 * j + 1];
+      v[2 * j] = a * t.c[j] - b * t.s[j];
+      v[2 * j + 1] = a * t.s[j] + b * t.c[j];
+    }
   }
 }
 
