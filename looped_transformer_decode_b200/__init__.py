@@ -18,6 +18,13 @@ from ._lib import (BF16, ERR_CUDA, ERR_INVALID, ERR_TOO_SMALL, ERR_UNSUPPORTED, 
                    STATUS_SLOT_RANGE, STATUS_TIMEOUT, Cfg, CQ8Cache, LLAError, RopeScaling, check,
                    last_error, lib)
 
+try:
+    from . import _binding          # needs torch and liblla.so loaded
+except ImportError as e:
+    raise ImportError(f"{e}: build the binding with `python -c \"import __graft_entry__ as g; "
+                      "g.build()\"`") from e
+_binding.set_error(LLAError)
+
 __all__ = [
     "Cfg", "LLAError", "MODE_PER_HEAD", "MODE_2D", "ratio", "cache_bytes", "codec_pack",
     "rope_table", "encode", "decode_workspace", "decode_attn", "decode_status", "lib",
@@ -94,9 +101,10 @@ def rope_table(cfg: Cfg, max_pos: int, device="cuda", out=None, scaling: RopeSca
         rd = cfg.d_rope or cfg.d_head                 # rotary dims
         out = torch.empty((max_pos, rd // 2, 2), dtype=torch.float32, device=device)
     if scaling is not None:
-        dev = _device(out)
-        _call(lib.lla_rope_table_scaled, dev, cfg.ref, ctypes.byref(scaling.c()), max_pos,
-              _dense(out, torch.float32, dev, "table"), out.numel() * 4)
+        with torch.cuda.device(out.device):
+            check(lib.lla_rope_table_scaled(cfg.ref, ctypes.byref(scaling.c()), max_pos,
+                                            _ptr(out, torch.float32, "table"), out.numel() * 4,
+                                            _stream()))
         return out
     check(lib.lla_rope_table(ctypes.byref(c), max_pos, _ptr(out, torch.float32, "table"),
                              out.numel() * 4, _stream()))
@@ -264,101 +272,6 @@ def full_decode_attn(cfg: Cfg, rope, ctx_len, q, k_self, v_self, q_pos, k_full, 
     return out
 
 
-# ---------------------------------------------------------------- lean argument passing
-#
-# A decode step makes these calls for every layer and loop, so the checks below cost a few
-# attribute reads per tensor; the detailed message is put together only when one fails.
-
-_F32, _BF16, _I32, _I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
-_ROW_TYPES = {_F32: F32, _BF16: BF16}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-def _device(t) -> int:
-    """CUDA device index of the tensor whose device the call runs on."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError("expected CUDA tensors")
-    return t.get_device()
-
-
-def _call(fn, dev: int, *args) -> None:
-    """fn(*args, stream) with ``dev`` current, on its current stream."""
-    if torch.cuda.current_device() == dev:
-        code = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            code = fn(*args, _raw_stream(dev))
-    if code:
-        check(code)
-
-
-def _refuse(t, dtype, dev, name, shape):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _dense(t, dtype, dev, name, shape=None) -> int:
-    """Address of a contiguous tensor of this type, device and shape."""
-    try:
-        if (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
-                and (shape is None or t.shape == shape)):
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _refuse(t, dtype, dev, name, shape)
-
-
-def _rows(t, dtype, dev, name, shape) -> int:
-    """Address of rows [n, heads, d] whose heads are contiguous; tokens may be strided."""
-    try:
-        if t.dtype is dtype and t.get_device() == dev and t.shape == shape:
-            n, heads, d = shape
-            if n == 0 or t.is_contiguous() or (
-                    t.stride(2) == 1 and (heads == 1 or t.stride(1) == d)):
-                return t.data_ptr()
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-    except AttributeError:
-        pass
-    _refuse(t, dtype, dev, name, shape)
-
-
-def _stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _row_type(t, name: str) -> int:
-    kind = _ROW_TYPES.get(getattr(t, "dtype", None))
-    if kind is None:
-        raise TypeError(f"{name} must be a float32 or bfloat16 tensor")
-    return kind
-
-
-def _layout(layout: str) -> int:
-    if layout not in ROPE_LAYOUTS:
-        raise ValueError(f"layout {layout!r} not in {sorted(ROPE_LAYOUTS)}")
-    return ROPE_LAYOUTS[layout]
-
-
-def _table(cfg: Cfg, rope, dev: int):
-    """(address, positions covered) of a rope table of cfg's rotary dims; (None, 0) without one."""
-    if rope is None:
-        return None, 0
-    if not isinstance(rope, torch.Tensor) or rope.dim() != 3:
-        raise ValueError("rope must be a table from rope_table, or None")
-    n = rope.shape[0]
-    return _dense(rope, _F32, dev, "rope", (n, (cfg.d_rope or cfg.d_head) // 2, 2)), n
-
-
 # ---------------------------------------------------------------- rotary positions
 
 def rope_apply(cfg: Cfg, rope, positions, x, layout: str = "half", inverse: bool = False, out=None,
@@ -369,20 +282,7 @@ def rope_apply(cfg: Cfg, rope, positions, x, layout: str = "half", inverse: bool
     strided (a slice of a fused projection); ``out`` may be ``x``.  ``inverse=True`` rotates back,
     which is the gradient with respect to x given the gradient of the output.
     """
-    kind, dev = _row_type(x, "x"), _device(x)
-    shape = x.shape
-    if len(shape) != 3 or shape[2] != cfg.d_head:
-        raise ValueError(f"x has shape {tuple(shape)}, expected (tokens, heads, {cfg.d_head})")
-    if rope is None:
-        raise ValueError("rope must be a table from rope_table")
-    if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    tp, tn = _table(cfg, rope, dev)
-    _call(lib.lla_rope_apply, dev, cfg.ref, tp, tn, _layout(layout), 1 if inverse else 0, kind,
-          shape[0], shape[1], _dense(positions, _I32, dev, "positions", shape[:1]),
-          _rows(x, x.dtype, dev, "x", shape), _stride(x), _rows(out, x.dtype, dev, "out", shape),
-          _stride(out), None if status is None else _dense(status, _I32, dev, "status"))
-    return out
+    return _binding.rope_apply(cfg, rope, positions, x, layout, inverse, out, status)
 
 
 # ---------------------------------------------------------------- pages
@@ -395,25 +295,8 @@ def page_map(page: int, ctx_len, n_new, block_table, free_list, n_free, tok_cap:
     ``n_free`` [1] (all int32) in place.  Returns (tok_start int32 [B + 1], slot int64 [tok_cap],
     positions int32 [tok_cap]) of the appended tokens.
     """
-    dev = _device(ctx_len)
-    if block_table.dim() != 2 or free_list.dim() != 1:
-        raise ValueError("block_table must be [B, max_pages] and free_list [n_pages]")
-    B, max_pages = block_table.shape
-    if tok_start is None:
-        tok_start = torch.empty((B + 1,), dtype=_I32, device=ctx_len.device)
-    if slot is None:
-        slot = torch.empty((tok_cap,), dtype=_I64, device=ctx_len.device)
-    if positions is None:
-        positions = torch.empty((tok_cap,), dtype=_I32, device=ctx_len.device)
-    _call(lib.lla_page_map, dev, B, page, max_pages, free_list.shape[0],
-          _dense(ctx_len, _I32, dev, "ctx_len", (B,)), _dense(n_new, _I32, dev, "n_new", (B,)),
-          _dense(block_table, _I32, dev, "block_table"), _dense(free_list, _I32, dev, "free_list"),
-          _dense(n_free, _I32, dev, "n_free", (1,)), tok_cap,
-          _dense(tok_start, _I32, dev, "tok_start", (B + 1,)),
-          _dense(slot, _I64, dev, "slot", (tok_cap,)),
-          _dense(positions, _I32, dev, "positions", (tok_cap,)),
-          None if status is None else _dense(status, _I32, dev, "status"))
-    return tok_start, slot, positions
+    return _binding.page_map(page, ctx_len, n_new, block_table, free_list, n_free, tok_cap,
+                             tok_start, slot, positions, status)
 
 
 # ---------------------------------------------------------------- paged 8-bit cache
@@ -434,24 +317,14 @@ class Q8Cache:
     def n_pages(self) -> int:
         return self.k.shape[0]
 
-    def ref(self, cfg: Cfg, dev: int):
-        """ctypes reference to the cache of this configuration on this device."""
-        n, H, page, d = self.k.shape
-        shape, rows = (n, cfg.H, page, cfg.d_head), (n, cfg.H)
-        return ctypes.byref(CQ8Cache(
-            _dense(self.k, torch.int8, dev, "cache.k", shape),
-            _dense(self.v, torch.int8, dev, "cache.v", shape),
-            _dense(self.k_scale, _F32, dev, "cache.k_scale", rows),
-            _dense(self.v_scale, _F32, dev, "cache.v_scale", rows), n, page))
-
 
 def q8_cache_alloc(cfg: Cfg, n_pages: int, page: int, device="cuda") -> Q8Cache:
     """Empty 8-bit cache of ``n_pages`` pages of ``page`` tokens (16, 32, 64 or 128)."""
     shape = (n_pages, cfg.H, page, cfg.d_head)
     return Q8Cache(torch.zeros(shape, dtype=torch.int8, device=device),
                    torch.zeros(shape, dtype=torch.int8, device=device),
-                   torch.zeros(shape[:2], dtype=_F32, device=device),
-                   torch.zeros(shape[:2], dtype=_F32, device=device))
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device))
 
 
 def q8_append(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, tok_start, positions, k, v,
@@ -462,17 +335,8 @@ def q8_append(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, tok_start, p
     ``tok_start`` as ``page_map`` leaves them.  Keys are rotated by ``rope`` at ``positions`` int32
     [n_tok]; with ``rope=None`` (then ``positions`` may be None) they come rotated.
     """
-    kind, dev = _row_type(k, "k"), _device(k)
-    B, max_pages = block_table.shape
-    shape = (k.shape[0], cfg.H, cfg.d_head)
-    tp, tn = _table(cfg, rope, dev)
-    _call(lib.lla_q8_append, dev, cfg.ref, cache.ref(cfg, dev), tp, tn, _layout(layout), kind, B,
-          max_pages, _dense(ctx_len, _I32, dev, "ctx_len", (B,)),
-          _dense(block_table, _I32, dev, "block_table"), shape[0],
-          _dense(tok_start, _I32, dev, "tok_start", (B + 1,)),
-          None if positions is None else _dense(positions, _I32, dev, "positions", shape[:1]),
-          _rows(k, k.dtype, dev, "k", shape), _stride(k), _rows(v, k.dtype, dev, "v", shape),
-          _stride(v), None if status is None else _dense(status, _I32, dev, "status"))
+    _binding.q8_append(cfg, rope, cache, ctx_len, block_table, tok_start, positions, k, v, layout,
+                       status)
 
 
 def q8_read(cfg: Cfg, cache: Q8Cache, slot, k_out=None, v_out=None, status=None):
@@ -480,17 +344,7 @@ def q8_read(cfg: Cfg, cache: Q8Cache, slot, k_out=None, v_out=None, status=None)
 
     A slot outside the cache leaves its row as it was (zeros without ``k_out`` / ``v_out``).
     """
-    dev = _device(slot)
-    shape = (slot.shape[0], cfg.H, cfg.d_head)
-    if k_out is None:
-        k_out = torch.zeros(shape, dtype=_BF16, device=slot.device)
-    if v_out is None:
-        v_out = torch.zeros(shape, dtype=_BF16, device=slot.device)
-    _call(lib.lla_q8_read, dev, cfg.ref, cache.ref(cfg, dev), shape[0],
-          _dense(slot, _I64, dev, "slot", shape[:1]), _dense(k_out, _BF16, dev, "k_out", shape),
-          _dense(v_out, _BF16, dev, "v_out", shape),
-          None if status is None else _dense(status, _I32, dev, "status"))
-    return k_out, v_out
+    return _binding.q8_read(cfg, cache, slot, k_out, v_out, status)
 
 
 def q8_decode_workspace(cfg: Cfg, B: int, n_cap: int, device="cuda"):
@@ -513,19 +367,5 @@ def q8_decode_attn(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, q, k_se
     ``rope=None``); ``k_self=v_self=None`` attends over the history alone.  Calls that may run at
     the same time need a workspace each.
     """
-    kind, dev = _row_type(q, "q"), _device(q)
-    B, max_pages = block_table.shape
-    rows, dtype = (B, cfg.H, cfg.d_head), q.dtype
-    if out is None:
-        out = torch.empty(rows, dtype=dtype, device=q.device)
-    if ws is None:
-        ws = q8_decode_workspace(cfg, B, max_pages * cache.page, q.device)
-    tp, tn = _table(cfg, rope, dev)
-    _call(lib.lla_q8_decode_attn, dev, cfg.ref, cache.ref(cfg, dev), tp, tn, _layout(layout), kind,
-          B, max_pages, _dense(ctx_len, _I32, dev, "ctx_len", (B,)),
-          _dense(block_table, _I32, dev, "block_table"), _dense(q, dtype, dev, "q", rows),
-          None if k_self is None else _dense(k_self, dtype, dev, "k_self", rows),
-          None if v_self is None else _dense(v_self, dtype, dev, "v_self", rows),
-          None if q_pos is None else _dense(q_pos, _I32, dev, "q_pos", (B,)),
-          _dense(out, dtype, dev, "out", rows), _dense(ws, torch.uint8, dev, "ws"), ws.numel())
-    return out
+    return _binding.q8_decode_attn(cfg, rope, cache, ctx_len, block_table, q, k_self, v_self, q_pos,
+                                   layout, out, ws)

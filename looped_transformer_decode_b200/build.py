@@ -1,7 +1,8 @@
-"""Build the in-tree CUDA library ``liblla.so`` for sm_100a with nvcc.
+"""Build the in-tree CUDA library ``liblla.so`` for sm_100a with nvcc, and the Python
+binding ``_binding.so`` of its later calls with g++.
 
-Objects go to ``_build/`` at the repository root; the shared library is written
-next to this file so that it travels with the package.  Rebuilds are
+Objects go to ``_build/`` at the repository root; the shared libraries are written
+next to this file so that they travel with the package.  Rebuilds are
 incremental on source/header modification times.
 """
 from __future__ import annotations
@@ -10,12 +11,14 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblla.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
@@ -54,7 +57,32 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if verbose:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
+    build_binding(verbose, force)
     return LIB
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    src = os.path.join(CSRC, "binding.cpp")
+    header = os.path.join(ROOT, "include", "lla.h")
+    if (not force and os.path.exists(BINDING)
+            and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), os.path.getmtime(header))):
+        return BINDING
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    dirs = [os.path.join(ROOT, "include"), *include_paths(), os.path.join(cuda, "include"),
+            sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{d}" for d in dirs), src, "-o", BINDING,
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-L" + PKG,
+           "-Wl,-rpath,$ORIGIN", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
+           "-lc10", "-lc10_cuda", "-l:liblla.so"]
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+    return BINDING
 
 
 if __name__ == "__main__":

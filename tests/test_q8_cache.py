@@ -165,6 +165,28 @@ def test_decode_refusals():
     assert lla.q8_decode_launches(cfg_of(2, 64), 4, -1) == -1
 
 
+def test_binding_refuses_what_is_not_on_a_gpu():
+    """The Python entry points name the argument, and no call reaches the library."""
+    cfg = cfg_of(2, 64)
+    x, one = torch.zeros((1, 2, 64)), torch.zeros(1, dtype=torch.int32)
+    cache = lla.q8_cache_alloc(cfg, 2, 16, device="cpu")
+    bt, slot = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int64)
+    calls = {
+        "x": lambda v: lla.rope_apply(cfg, torch.zeros((4, 32, 2)), one, v),
+        "k": lambda v: lla.q8_append(cfg, None, cache, one, bt, one, None, v, v),
+        "q": lambda v: lla.q8_decode_attn(cfg, None, cache, one, bt, v, None, None, None),
+    }
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match=f"{name} must be a CUDA tensor"):
+            call(x)
+        with pytest.raises(TypeError, match=f"{name} must be a torch.Tensor"):
+            call([1.0])
+    with pytest.raises(ValueError, match="slot must be a CUDA tensor"):
+        lla.q8_read(cfg, cache, slot)
+    with pytest.raises(ValueError, match="ctx_len must be a CUDA tensor"):
+        lla.page_map(16, one, one, bt, one, one, 4)
+
+
 # ----------------------------------------------------------------------------- GPU: append and read
 
 def random_cache(g, cfg, n_pages, page):
@@ -523,6 +545,18 @@ def test_python_argument_checks():
         lla.q8_append(cfg, None, cache, one.cpu(), bt, i32([0, 1]), None, q, q)
     with pytest.raises(ValueError):
         lla.q8_append(cfg, None, cache, one, bt, i32([0, 1]), None, q.transpose(1, 2), q)
+    with pytest.raises(ValueError, match="layout"):
+        lla.q8_append(cfg, None, cache, one, bt, i32([0, 1]), None, q, q, layout="both")
+    with pytest.raises(ValueError, match="heads of a token must be contiguous"):
+        lla.rope_apply(cfg, lla.rope_table(cfg, 4), one, torch.zeros((1, 2, 128), device="cuda")[..., ::2])
+    with pytest.raises(TypeError, match="slot must be torch.int64"):
+        lla.q8_read(cfg, cache, one)
+    with pytest.raises(lla.LLAError) as e:
+        lla.q8_decode_attn(cfg, None, cache, one, bt, q, None, None, None,
+                           ws=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == lla.ERR_TOO_SMALL and "workspace" in str(e.value)
+    with pytest.raises(AttributeError):
+        lla.q8_read(None, cache, torch.zeros(1, dtype=torch.int64, device="cuda"))
 
 
 # ----------------------------------------------------------------------------- GPU: together
