@@ -543,6 +543,7 @@ int lla_q8_decode_launches(const lla_cfg* cfg, int32_t B, int32_t n_cap);
  * Tokens of a page outside the cache are left out (LLA_STATUS_PAGE_RANGE); what the cache
  * holds past ctx_len[b] or in pages of other sequences does not reach the output.
  * Scores, softmax and sums are held in fp32 or exact integers.
+ * B <= 65535; B * H * (max_pages * page / 32 + 16) at most 2^31 - 4097 (LLA_ERR_UNSUPPORTED).
  */
 int lla_q8_decode_attn(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
                        int32_t rope_max_pos, int32_t layout, int32_t dtype, int32_t B,

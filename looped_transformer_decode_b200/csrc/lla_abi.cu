@@ -878,9 +878,9 @@ int lla_q8_decode_attn(const lla_cfg* cfg, const lla_q8_cache* cache, const void
   e = check_batch("lla_q8_decode_attn", B, max_pages, cache->page);
   if (e) return e;
   if (rope_table && rope_max_pos < 1) return fail(LLA_ERR_INVALID, "rope_max_pos must be >= 1");
-  if ((int64_t)B * cfg->H * ((int64_t)max_pages * cache->page / 32 + 16) > INT32_MAX)
+  if ((int64_t)B * cfg->H * ((int64_t)max_pages * cache->page / 32 + 16) > INT32_MAX - 4096)
     return fail(LLA_ERR_UNSUPPORTED,
-                "lla_q8_decode_attn: B * H * (max_pages * page / 32 + 16) above 2^31-1");
+                "lla_q8_decode_attn: B * H * (max_pages * page / 32 + 16) above 2^31 - 4097");
   if (B == 0) return ok();
   if (!ctx_len || (max_pages && !block_table) || !q || !out || !ws || (rope_table && !q_pos))
     return fail(LLA_ERR_INVALID, "lla_q8_decode_attn: NULL pointer argument");

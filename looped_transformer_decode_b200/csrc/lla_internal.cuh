@@ -161,7 +161,7 @@ struct FullDecodeParams {
   const float2* rope;
   float* out;
   float* partials;                 // [B][H][S][2 + d] when S > 1
-  int32_t* status;                 // ws words [0], [1]
+  int32_t* status;                 // ws words [0] (not used), [1]
   uint32_t* counter;               // ws word [4]: CTAs finished in this call
 };
 struct FullPlan {
@@ -239,6 +239,9 @@ struct Q8ReadArgs {
   __nv_bfloat16* v_out;
   int32_t* status;
 };
+struct Q8Divisor {
+  uint32_t factor, shift;
+};
 struct Q8DecodeArgs {
   const float2* rope;              // null: q and k_self come rotated
   int rope_max_pos, layout, d, rd, H, bf16;
@@ -256,9 +259,10 @@ struct Q8DecodeArgs {
   const float* vs;
   void* out;
   int32_t* status;                 // ws words [0], [1]
-  uint32_t* counter;               // ws word [4]: blocks finished in this call
+  uint32_t* counter;               // ws word [4]: blocks finished in this call, status bits above
   uint32_t* piece_counters;        // [blocks]: pieces of the item that a block's range begins
   float* partials;                 // [blocks][2][2 + d]
+  Q8Divisor by_grid, by_warps;     // the launch's blocks and warps
 };
 cudaError_t launch_q8_append(const Q8AppendArgs& a, cudaStream_t s);
 cudaError_t launch_q8_read(Q8ReadArgs a, cudaStream_t s);

@@ -101,12 +101,36 @@ __device__ __forceinline__ void load_words(const unsigned char* p, uint32_t* w) 
   }
 }
 
+// The call's counter word: blocks that finished, and the status bits above them, so that the
+// last block learns of every bit from the count that it must read anyway.
+constexpr int kQ8StatusShift = 16;
+__device__ __forceinline__ void tell_status(const Q8DecodeArgs& a, uint32_t bits) {
+  atomicOr(a.counter, bits << kQ8StatusShift);
+}
+
+// Largest of the lanes' values.
+__device__ __forceinline__ float warp_largest(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// a / b for the invariant divisor of `by`, a < 2^31.
+__device__ __forceinline__ uint32_t divide(uint32_t a, const Q8Divisor& by) {
+  return by.factor ? __umulhi(a, by.factor) >> by.shift : a;
+}
+
+// Pieces of up to about 1 / inv_q tiles, at most `most` of them.
+__device__ __forceinline__ uint32_t pieces_of(uint32_t tiles, float inv_q, uint32_t most) {
+  return max(1, (int)ceilf(fminf((float)tiles * inv_q, (float)most)));
+}
+
 // Length of sequence b, clamped into its block table.
 __device__ __forceinline__ int q8_length(const Q8DecodeArgs& a, int b, bool tell) {
   const long long cap = (long long)a.max_pages << a.shift;
   const int n = a.ctx_len[b];
   if (n >= 0 && n <= cap) return n;
-  if (tell) atomicOr(a.status, LLA_STATUS_CTX_RANGE);
+  if (tell) tell_status(a, LLA_STATUS_CTX_RANGE);
   return n < 0 ? 0 : (int)cap;
 }
 
@@ -128,7 +152,8 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   __shared__ unsigned long long sums3[kQ8Warps];
   __shared__ uint32_t start_at[kQ8Warps];   // units (aligned: pieces) before the sequence
   __shared__ int start_b[kQ8Warps];         // of a block's, or warp's, first item
-  __shared__ int abort_word, is_last, told;
+  __shared__ int start_n;                   // its length (aligned)
+  __shared__ int abort_word, is_last;
   volatile int* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
   unsigned char* ring = sm + warp * S::kRing;
@@ -156,10 +181,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     mine += tiles;
     most = max(most, tiles);
   }
-  if (tid == 0) {
-    abort_word = 0;
-    told = 0;
-  }
+  if (tid == 0) abort_word = 0;
   if (lane == 0) {
     for (int s = 0; s < kQ8Stages; ++s) sm100::mbar_init(&bars[s], 1);
     sm100::fence_mbar_init();
@@ -187,22 +209,25 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   const uint32_t H = a.H, items = a.B * H, grid = gridDim.x, warps = grid * kQ8Warps;
   const uint32_t block_units = (total + a.B * kQ8ItemBlock) * H;
   const uint32_t warp_units = (total + a.B * kQ8ItemWarp) * H;
-  const uint32_t in_turn = (items + warps - 1) / warps;          // items of one warp
-  const uint32_t warp_cost = min(in_turn * (most + kQ8ItemWarp), warp_units / warps + most);
-  uint32_t block_cost = block_units / warps + kQ8ItemBlock / 2;
+  const uint32_t in_turn = divide(items + warps - 1, a.by_warps);   // items of one warp
+  const uint32_t warp_cost = min(in_turn * (most + kQ8ItemWarp), divide(warp_units, a.by_warps) + most);
+  uint32_t block_cost = divide(block_units, a.by_warps) + kQ8ItemBlock / 2;
   uint32_t q = 0, blocks = 0, start_pieces = 0, mine_pieces = 0;
+  float inv_q = 0.f;                        // 1 / q, and a little less (aligned)
   bool aligned = false;
   if (items <= grid) {
     // pieces for three q, in fields of 21 bits: at most 444 sequences of 445 pieces
-    const uint32_t q0 = max((uint32_t)kQ8MinTiles, (total * H + grid - 1) / grid);
+    const uint32_t q0 = max((uint32_t)kQ8MinTiles, divide(total * H + grid - 1, a.by_grid));
+    float inv[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+      inv[j] = (1.f - 0x1p-20f) / (float)(q0 + j * kQ8ItemBlock / 2);
     unsigned long long v = 0;
     for (int b = seg0; b < seg1; ++b) {
       const uint32_t tiles = tiles_of(q8_length(a, b, false));
 #pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const uint32_t qj = q0 + j * kQ8ItemBlock / 2;
-        v += (unsigned long long)min((tiles + qj - 1) / qj, grid + 1) << (21 * j);
-      }
+      for (int j = 0; j < 3; ++j)
+        v += (unsigned long long)pieces_of(tiles, inv[j], grid + 1) << (21 * j);
     }
     unsigned long long upto = v;
 #pragma unroll
@@ -226,6 +251,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       if (n * H <= grid) {
         aligned = true;
         q = q0 + j * kQ8ItemBlock / 2;
+        inv_q = inv[j];
         blocks = n * H;
         start_pieces = (uint32_t)(upto >> (21 * j)) & kField;
         mine_pieces = (uint32_t)(v >> (21 * j)) & kField;
@@ -237,10 +263,10 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   const uint32_t units = by_warp ? warp_units : block_units;
   if (by_warp) {
     aligned = false;
-    q = (units + warps - 1) / warps;
+    q = divide(units + warps - 1, a.by_warps);
     blocks = (units + kQ8Warps * q - 1) / (kQ8Warps * q);
   } else if (!aligned) {
-    q = max((uint32_t)kQ8MinTiles, (units + grid - 1) / grid);
+    q = max((uint32_t)kQ8MinTiles, divide(units + grid - 1, a.by_grid));
     blocks = (units + q - 1) / q;
   }
   if (c >= blocks) return;
@@ -259,12 +285,13 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       int b = seg0;
       for (; b < seg1 - 1; ++b) {
         const uint32_t tiles = tiles_of(q8_length(a, b, false));
-        const uint32_t len = (aligned ? (tiles + q - 1) / q : tiles + extra) * H;
+        const uint32_t len = (aligned ? pieces_of(tiles, inv_q, grid + 1) : tiles + extra) * H;
         if (x < at + len) break;
         at += len;
       }
       start_b[w] = b;
       start_at[w] = at;
+      if (aligned) start_n = q8_length(a, b, false);
     }
   }
   __syncthreads();
@@ -282,12 +309,15 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   // the item that unit u lies in, or the block's piece (aligned); false: there is none
   auto find_item = [&]() {
     if (aligned) {
-      it.n = q8_length(a, it.b, false);
-      const uint32_t tiles = tiles_of(it.n), pieces = (tiles + q - 1) / q, k = c - seq_at;
-      it.h = k / pieces;
-      const uint32_t part = k - it.h * pieces, base = tiles / pieces, rem = tiles - base * pieces;
-      it.t0 = part * base + min(part, rem);
-      it.t1 = it.t0 + base + (part < rem ? 1 : 0);
+      it.n = start_n;
+      const uint32_t tiles = tiles_of(it.n), pieces = pieces_of(tiles, inv_q, grid + 1);
+      const uint32_t k = c - seq_at;                // below 2^18 here, as c is
+      const float inv = __frcp_rn((float)pieces);
+      it.h = (int)(((float)k + 0.5f) * inv);
+      const uint32_t part = k - it.h * pieces;
+      const float each = (float)tiles * inv;
+      it.t0 = (int)((float)part * each);
+      it.t1 = part + 1 == pieces ? tiles : (uint32_t)((float)(part + 1) * each);
       it.c0 = c - part;
       it.pieces = pieces;
       it.slot = it.first_slot = 0;
@@ -381,11 +411,8 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     vs0 = scale_of(a.vs, id0);
   };
   bool more = find_item(), started = false;
-  unsigned finished = 0;                                       // blocks that finished before
-  auto finish_block = [&]() {
-    if (told || c == 0) __threadfence();                       // block 0 tells of lengths
-    return atomicAdd(a.counter, 1u);
-  };
+  uint32_t finished = 0;                                       // the counter word before
+  auto finish_block = [&]() { return atomicAdd(a.counter, 1u); };
   if (more) load_ids();
   while (more) {
     const int first = it.t0 + lead;
@@ -398,28 +425,27 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       const bool turn = a.rope != nullptr;
       const RowChunk rc = row_chunk<8>(lane, D, turn ? a.rd : 0, a.layout);
       float v[8], k[8];
-      int asked = 0;
+      Turn<8> angles;
+      const bool rotates = turn && lane < D / 8 && rc.rotary;
       if (lane < D / 8) {
+        int asked = 0;
         if (turn) asked = a.q_pos[it.b];
         load_chunk<8>(static_cast<const T*>(a.q) + bh * D, rc, v);
         if (a.k_self) load_chunk<8>(static_cast<const T*>(a.k_self) + bh * D, rc, k);
+        if (turn) {
+          const int pos = checked_position(asked, a.rope_max_pos, nullptr, false);
+          if (lane == 0 && pos != asked) tell_status(a, LLA_STATUS_POSITION_RANGE);
+          if (rotates) angles = load_turn<8>(a.rope + (size_t)pos * (a.rd / 2), rc);
+        }
       }
-      if (!started) start_copies();
+      if (!started) start_copies();                             // while the angles come
       started = true;
       if (lane < D / 8) {
         if (a.k_self) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) self = fmaf(v[j], k[j], self);
         }
-        if (turn) {
-          const int pos = checked_position(asked, a.rope_max_pos, nullptr, false);
-          if (lane == 0 && pos != asked) {
-            atomicOr(a.status, LLA_STATUS_POSITION_RANGE);
-            told = 1;
-          }
-          if (rc.rotary)
-            rotate_chunk<8>(load_turn<8>(a.rope + (size_t)pos * (a.rd / 2), rc), rc.split, v);
-        }
+        if (rotates) rotate_chunk<8>(angles, rc.split, v);
         store_chunk<8>(qs, rc, v);
       }
     }
@@ -442,8 +468,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
         strange |= !(fabsf(v[j]) <= FLT_MAX);
       }
       strange = __any_sync(0xffffffffu, strange);               // and the values are read
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      amax = warp_largest(amax);
       constexpr float kTop = 127.f * 16384.f;
       const float inv = amax > kQ8Tiny ? kTop / amax : 0.f;
       score_scale = strange ? 0.f : a.kappa * amax / kTop;      // strange: pl becomes NaN below
@@ -569,9 +594,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
         }
         if (__any_sync(0xffffffffu, above)) {
           float mt = S::kScores == 2 ? fmaxf(sc[0], sc[S::kScores - 1]) : sc[0];
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1)
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
+          mt = warp_largest(mt);
           const float f = exp2_down(m - mt);                    // 0 the first time
           m = mt;
           l *= f;
@@ -587,9 +610,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
         }
         if (__any_sync(0xffffffffu, heavy)) {
           float top = S::kScores == 2 ? fmaxf(vsc[0], vsc[S::kScores - 1]) : vsc[0];
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          top = warp_largest(top);
           if (top > R) {
             flush();
             R = top;
@@ -649,15 +670,9 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       vs0 = vs1;
     }
     if (it.t1 > first) used += (it.t1 - first + step - 1) / step;
-    if (__any_sync(0xffffffffu, bad) && lane == 0) {
-      atomicOr(a.status, LLA_STATUS_PAGE_RANGE);
-      told = 1;
-    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) tell_status(a, LLA_STATUS_PAGE_RANGE);
     bad = false;
-    if (aborted && lane == 0) {
-      atomicOr(a.status, LLA_STATUS_TIMEOUT);
-      told = 1;
-    }
+    if (aborted && lane == 0) tell_status(a, LLA_STATUS_TIMEOUT);
     // the next item's first tiles are on their way while this one is merged
     const Q8Item now = it;
     more = !aligned && find_item();
@@ -787,22 +802,31 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     }
     __syncthreads();                                            // parts and is_last are free
   }
-  // the last block to finish publishes the call's status word and re-arms the counter
+  // the last block to finish publishes the call's status and re-arms the counter
   if (by_warp || !started) {                                   // also a range without a tile
     __syncthreads();
     if (tid == 0) finished = finish_block();
   }
-  if (tid == 0 && finished == blocks - 1) {
-    __threadfence();
-    a.status[1] = atomicExch(&a.status[0], 0);
-    atomicExch(a.counter, 0u);
+  if (tid == 0 && (finished & ((1u << kQ8StatusShift) - 1)) == blocks - 1) {
+    a.status[1] = finished >> kQ8StatusShift;
+    *a.counter = 0;
   }
+}
+
+// For d > 1, with 2^k < d <= 2^(k + 1) and factor = ceil(2^(32 + k) / d), factor * d exceeds 2^(32 + k) by
+// less than 2^(k + 1), which is too little to carry a quotient of a < 2^31 to the next integer.
+Q8Divisor divisor(uint32_t d) {
+  Q8Divisor r{0, 0};
+  if (d == 1) return r;                     // factor 0: divides by one
+  while ((2u << r.shift) < d) ++r.shift;
+  r.factor = (uint32_t)(((1ull << (32 + r.shift)) + d - 1) / d);
+  return r;
 }
 
 int q8_max_blocks() { return sm_count() * kQ8BlocksPerSm; }
 
 template <typename T, int D>
-cudaError_t launch_decode_td(const Q8DecodeArgs& a, cudaStream_t s) {
+cudaError_t launch_decode_td(Q8DecodeArgs a, cudaStream_t s) {
   using S = Q8Shape<D>;
   cudaError_t e = cudaFuncSetAttribute(q8_decode_kernel<T, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
@@ -812,6 +836,8 @@ cudaError_t launch_decode_td(const Q8DecodeArgs& a, cudaStream_t s) {
   // at most one block per kQ8MinTiles tiles of every item
   const long long per_item = std::max(1LL, (tiles + kQ8MinTiles - 1) / kQ8MinTiles);
   const long long grid = std::min<long long>((long long)a.B * a.H * per_item, q8_max_blocks());
+  a.by_grid = divisor((uint32_t)grid);
+  a.by_warps = divisor((uint32_t)grid * kQ8Warps);
   q8_decode_kernel<T, D><<<(unsigned)grid, kQ8Threads, S::kBytes, s>>>(a);
   return cudaGetLastError();
 }
