@@ -31,9 +31,8 @@ namespace {
 
 constexpr int kQ8Warps = 4;
 constexpr int kQ8Threads = 32 * kQ8Warps;
-constexpr int kQ8BlocksPerSm = 3;
 constexpr int kQ8Stages = 2;
-constexpr int kQ8MinTiles = 4;              // tiles worth a block
+constexpr int kQ8MinTiles = 8;              // tiles worth a block
 constexpr int kQ8ItemBlock = 12;            // start and merge of an item in tiles, for a block
 constexpr int kQ8ItemWarp = 4;              // and for a warp that has it to itself
 constexpr int kQ8FlushTiles = 4096;         // 2 * 4 * 255 * 128 per tile and dim stays below 2^31
@@ -46,6 +45,10 @@ struct Q8Shape {
   // four of them are a group, the unit of the arithmetic.  kSubs 16-token blocks, each in
   // one page, make a group; two groups make a tile.
   static constexpr int kLanes = D == 96 ? 8 : D / 16;
+  // Registers bound the blocks per SM.  Two take 250 a thread and hold both groups' values;
+  // three of 168 spill (256 sequences of 4096 tokens, 16 heads of 128: 644 us against 687) but
+  // for 96, whose lanes hold 12 codes.
+  static constexpr int kBlocksPerSm = D == 96 ? 3 : 2;
   static constexpr int kWords = D / kLanes / 4;             // 4-code words per lane and row
   static constexpr int kRows = 32 / kLanes;
   static constexpr int kGroup = 4 * kRows;
@@ -142,7 +145,8 @@ struct Q8Item {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q8DecodeArgs a) {
+__global__ void __launch_bounds__(kQ8Threads, Q8Shape<D>::kBlocksPerSm)
+q8_decode_kernel(Q8DecodeArgs a) {
   using S = Q8Shape<D>;
   constexpr int W = S::kWords;
   extern __shared__ __align__(128) unsigned char sm[];
@@ -210,7 +214,8 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   const uint32_t block_units = (total + a.B * kQ8ItemBlock) * H;
   const uint32_t warp_units = (total + a.B * kQ8ItemWarp) * H;
   const uint32_t in_turn = divide(items + warps - 1, a.by_warps);   // items of one warp
-  const uint32_t warp_cost = min(in_turn * (most + kQ8ItemWarp), divide(warp_units, a.by_warps) + most);
+  const uint32_t warp_cost =
+      min(in_turn * (most + kQ8ItemWarp), divide(warp_units, a.by_warps) + most);
   uint32_t block_cost = divide(block_units, a.by_warps) + kQ8ItemBlock / 2;
   uint32_t q = 0, blocks = 0, start_pieces = 0, mine_pieces = 0;
   float inv_q = 0.f;                        // 1 / q, and a little less (aligned)
@@ -365,7 +370,8 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   auto part_id = [&](int t) {
     if (lane >= S::kParts || t >= it.t1) return -1;
     const int tok = t * S::kTile + lane * 16;                  // lengths stay below 2^31
-    return tok < it.n ? __ldg(a.block_table + (long long)it.b * a.max_pages + (tok >> a.shift)) : -1;
+    if (tok >= it.n) return -1;
+    return __ldg(a.block_table + (long long)it.b * a.max_pages + (tok >> a.shift));
   };
   auto checked = [&](int t, int id) {                          // -1 for what is not there
     const bool there = lane < S::kParts && t < it.t1 && t * S::kTile + lane * 16 < it.n;
@@ -413,8 +419,34 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   bool more = find_item(), started = false;
   uint32_t finished = 0;                                       // the counter word before
   auto finish_block = [&]() { return atomicAdd(a.counter, 1u); };
-  if (more) load_ids();
+  // q, the in-flight token's key and their angles, eight dims a lane: the next item's are
+  // loaded before the merge of the one before it
+  const bool turn = a.rope != nullptr, chunk = lane < D / 8;
+  const RowChunk rc = row_chunk<8>(lane, D, turn ? a.rd : 0, a.layout);
+  float v[8], k[8];
+  Turn<8> angles;
+  int asked = 0;
+  auto fetch_q = [&]() {
+    if (!chunk) return;
+    const size_t row = ((size_t)it.b * a.H + it.h) * D;
+    if (turn) asked = a.q_pos[it.b];
+    load_chunk<8>(static_cast<const T*>(a.q) + row, rc, v);
+    if (a.k_self) load_chunk<8>(static_cast<const T*>(a.k_self) + row, rc, k);
+  };
+  auto fetch_angles = [&]() {
+    if (!chunk || !turn) return;
+    const int pos = checked_position(asked, a.rope_max_pos, nullptr, false);
+    if (lane == 0 && pos != asked) tell_status(a, LLA_STATUS_POSITION_RANGE);
+    if (rc.rotary) angles = load_turn<8>(a.rope + (size_t)pos * (a.rd / 2), rc);
+  };
+  if (more) {
+    load_ids();
+    fetch_q();
+    fetch_angles();
+    start_copies();                                            // while the angles come
+  }
   while (more) {
+    started = true;
     const int first = it.t0 + lead;
     const size_t bh = (size_t)it.b * a.H + it.h;
 
@@ -422,30 +454,12 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     // token's score, which needs no rotation, both sitting at q_pos
     float self = 0.f;
     {
-      const bool turn = a.rope != nullptr;
-      const RowChunk rc = row_chunk<8>(lane, D, turn ? a.rd : 0, a.layout);
-      float v[8], k[8];
-      Turn<8> angles;
-      const bool rotates = turn && lane < D / 8 && rc.rotary;
-      if (lane < D / 8) {
-        int asked = 0;
-        if (turn) asked = a.q_pos[it.b];
-        load_chunk<8>(static_cast<const T*>(a.q) + bh * D, rc, v);
-        if (a.k_self) load_chunk<8>(static_cast<const T*>(a.k_self) + bh * D, rc, k);
-        if (turn) {
-          const int pos = checked_position(asked, a.rope_max_pos, nullptr, false);
-          if (lane == 0 && pos != asked) tell_status(a, LLA_STATUS_POSITION_RANGE);
-          if (rotates) angles = load_turn<8>(a.rope + (size_t)pos * (a.rd / 2), rc);
-        }
-      }
-      if (!started) start_copies();                             // while the angles come
-      started = true;
-      if (lane < D / 8) {
+      if (chunk) {
         if (a.k_self) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) self = fmaf(v[j], k[j], self);
         }
-        if (rotates) rotate_chunk<8>(angles, rc.split, v);
+        if (rc.rotary) rotate_chunk<8>(angles, rc.split, v);
         store_chunk<8>(qs, rc, v);
       }
     }
@@ -548,60 +562,62 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
       if (++since >= kQ8FlushTiles) flush();
       const unsigned char* st = ring + s * S::kStage + r * D + col * 4 * W;
       const int rows_left = it.n - t * S::kTile - r - S::kRows * i_own;   // of a lane's first score
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (!(live >> (g * S::kSubs) & ((1 << S::kSubs) - 1))) continue;  // warp-uniform
-        const unsigned char* kp = st + g * S::kSubs * S::kPartBytes;
-        float part[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t kw[W];
-          load_words<W>(kp + i * S::kRows * D, kw);
-          int s1 = 0, s2 = 0, s3 = 0;
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            s1 = __dp4a((int)kw[w], (int)q1[w], s1);
-            s2 = __dp4a((int)kw[w], (int)q2[w], s2);
-            s3 = __dp4a((int)kw[w], (int)q3[w], s3);
-          }
-          part[i] = fmaf((float)(s1 * 128 + s2), 128.f, (float)s3);
-        }
-        // sums over a row's lanes, each exchange halving what a lane holds
+      if (live) {                                               // else no page of it is there
+        // Scores of both groups, then one look at their maxima, then the weights: the groups' long
+        // chains of exchanges run side by side.
         constexpr int kFar = S::kLanes / 2, kNear = S::kLanes / 4;
-        const bool upper = col & kFar;
-        float x[2];
-        x[0] = (upper ? part[2] : part[0]) +
-               __shfl_xor_sync(0xffffffffu, upper ? part[0] : part[2], kFar);
-        x[1] = (upper ? part[3] : part[1]) +
-               __shfl_xor_sync(0xffffffffu, upper ? part[1] : part[3], kFar);
-        if constexpr (S::kLanes >= 4) {
-          const bool odd = col & kNear;
-          x[0] = (odd ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], kNear);
-        }
-        if constexpr (S::kLanes == 8) x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
-        float sc[S::kScores], vsc[S::kScores];
+        const bool upper = col & kFar, odd = col & kNear;
+        float sc[2][S::kScores], vsc[2][S::kScores];
         bool above = false, heavy = false;
 #pragma unroll
-        for (int k = 0; k < S::kScores; ++k) {
-          // the 16-token block of the group that the row lies in
-          const int sub = g * S::kSubs + (S::kSubs == 1 ? 0 : S::kSubs == 2 ? i_own >> 1 : i_own + k);
-          const float ksc = __shfl_sync(0xffffffffu, ks0, sub) * score_scale;
-          vsc[k] = __shfl_sync(0xffffffffu, vs0, sub);
-          const bool there = rows_left > g * S::kGroup + k * S::kRows && (live >> sub & 1);
-          sc[k] = there ? x[k] * ksc : -INFINITY;
-          above |= sc[k] > m;
-          heavy |= vsc[k] > R;                                  // weights are at most vs: p <= 1
+        for (int g = 0; g < 2; ++g) {
+          const unsigned char* kp = st + g * S::kSubs * S::kPartBytes;
+          float part[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t kw[W];
+            load_words<W>(kp + i * S::kRows * D, kw);
+            int s1 = 0, s2 = 0, s3 = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+              s1 = __dp4a((int)kw[w], (int)q1[w], s1);
+              s2 = __dp4a((int)kw[w], (int)q2[w], s2);
+              s3 = __dp4a((int)kw[w], (int)q3[w], s3);
+            }
+            part[i] = fmaf((float)(s1 * 128 + s2), 128.f, (float)s3);
+          }
+          // sums over a row's lanes, each exchange halving what a lane holds
+          float x[2];
+          x[0] = (upper ? part[2] : part[0]) +
+                 __shfl_xor_sync(0xffffffffu, upper ? part[0] : part[2], kFar);
+          x[1] = (upper ? part[3] : part[1]) +
+                 __shfl_xor_sync(0xffffffffu, upper ? part[1] : part[3], kFar);
+          if constexpr (S::kLanes >= 4)
+            x[0] = (odd ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], kNear);
+          if constexpr (S::kLanes == 8) x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+#pragma unroll
+          for (int k = 0; k < S::kScores; ++k) {
+            // the 16-token block of the group that the row lies in
+            const int sub = g * S::kSubs + (S::kSubs == 1 ? 0 : S::kSubs == 2 ? i_own >> 1 : i_own + k);
+            const float ksc = __shfl_sync(0xffffffffu, ks0, sub) * score_scale;
+            vsc[g][k] = __shfl_sync(0xffffffffu, vs0, sub);
+            const bool there = rows_left > g * S::kGroup + k * S::kRows && (live >> sub & 1);
+            sc[g][k] = there ? x[k] * ksc : -INFINITY;
+            above |= sc[g][k] > m;
+            heavy |= vsc[g][k] > R;                               // weights are at most vs: p <= 1
+          }
         }
         if (__any_sync(0xffffffffu, above)) {
-          float mt = S::kScores == 2 ? fmaxf(sc[0], sc[S::kScores - 1]) : sc[0];
+          float mt = fmaxf(fmaxf(sc[0][0], sc[0][S::kScores - 1]),
+                           fmaxf(sc[1][0], sc[1][S::kScores - 1]));
           mt = warp_largest(mt);
-          const float f = exp2_down(m - mt);                    // 0 the first time
+          const float f = exp2_down(m - mt);                      // 0 the first time
           m = mt;
           l *= f;
           R *= f;
 #pragma unroll
           for (int j = 0; j < 4 * W; ++j) o[j] *= f;
-          if (R < kQ8SmallRef) {                                // 1 / R stays finite
+          if (R < kQ8SmallRef) {                                  // 1 / R stays finite
             flush();
             R = kQ8SmallRef;
           }
@@ -609,7 +625,8 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
           heavy = true;
         }
         if (__any_sync(0xffffffffu, heavy)) {
-          float top = S::kScores == 2 ? fmaxf(vsc[0], vsc[S::kScores - 1]) : vsc[0];
+          float top = fmaxf(fmaxf(vsc[0][0], vsc[0][S::kScores - 1]),
+                            fmaxf(vsc[1][0], vsc[1][S::kScores - 1]));
           top = warp_largest(top);
           if (top > R) {
             flush();
@@ -617,47 +634,55 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
             wf = kQ8Weight / R;
           }
         }
-        uint32_t wt[S::kScores];
-#pragma unroll
-        for (int k = 0; k < S::kScores; ++k) {
-          const float p = exp2_down(sc[k] - m);
-          l += p;
-          wt[k] = __float2uint_rn(p * (vsc[k] * wf));
-        }
-        // the weights of a lane's four rows, then their bytes: hi, mid, lo words of four tokens
-        uint32_t e0 = wt[0], e1 = wt[S::kScores - 1];
-        if constexpr (S::kLanes >= 4) {
-          const uint32_t other = __shfl_xor_sync(0xffffffffu, wt[0], kNear);
-          const bool odd = col & kNear;
-          e0 = odd ? other : wt[0];
-          e1 = odd ? wt[0] : other;
-        }
-        const uint32_t f0 = __shfl_xor_sync(0xffffffffu, e0, kFar);
-        const uint32_t f1 = __shfl_xor_sync(0xffffffffu, e1, kFar);
-        const uint32_t g0 = upper ? f0 : e0, g1 = upper ? f1 : e1;
-        const uint32_t g2 = upper ? e0 : f0, g3 = upper ? e1 : f1;
-        const uint32_t a01 = __byte_perm(g0, g1, 0x5140), a23 = __byte_perm(g2, g3, 0x5140);
-        const uint32_t h01 = __byte_perm(g0, g1, 0x0062), h23 = __byte_perm(g2, g3, 0x0062);
-        const uint32_t wlo = __byte_perm(a01, a23, 0x5410), wmid = __byte_perm(a01, a23, 0x7632);
-        const uint32_t whi = __byte_perm(h01, h23, 0x5410);
         held = true;
-        uint32_t vw[4][W];
+        uint32_t whi[2], wmid[2], wlo[2];     // bytes of the weights of a lane's four rows
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_words<W>(kp + S::kHalf + i * S::kRows * D, vw[i]);
+        for (int g = 0; g < 2; ++g) {
+          uint32_t wt[S::kScores];
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          // four rows of four dims, turned into four dims of four rows
-          const uint32_t y0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
-          const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-          const uint32_t y2 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-          const uint32_t y3 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-          const uint32_t dim[4] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632),
-                                   __byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
+          for (int k = 0; k < S::kScores; ++k) {
+            const float p = exp2_down(sc[g][k] - m);
+            l += p;
+            wt[k] = __float2uint_rn(p * (vsc[g][k] * wf));
+          }
+          uint32_t e0 = wt[0], e1 = wt[S::kScores - 1];
+          if constexpr (S::kLanes >= 4) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, wt[0], kNear);
+            e0 = odd ? other : wt[0];
+            e1 = odd ? wt[0] : other;
+          }
+          const uint32_t f0 = __shfl_xor_sync(0xffffffffu, e0, kFar);
+          const uint32_t f1 = __shfl_xor_sync(0xffffffffu, e1, kFar);
+          const uint32_t g0 = upper ? f0 : e0, g1 = upper ? f1 : e1;
+          const uint32_t g2 = upper ? e0 : f0, g3 = upper ? e1 : f1;
+          const uint32_t a01 = __byte_perm(g0, g1, 0x5140), a23 = __byte_perm(g2, g3, 0x5140);
+          const uint32_t h01 = __byte_perm(g0, g1, 0x0062), h23 = __byte_perm(g2, g3, 0x0062);
+          wlo[g] = __byte_perm(a01, a23, 0x5410);
+          wmid[g] = __byte_perm(a01, a23, 0x7632);
+          whi[g] = __byte_perm(h01, h23, 0x5410);
+        }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc1[4 * w + j] = dp4a_us(whi, dim[j], acc1[4 * w + j]);
-            acc2[4 * w + j] = dp4a_us(wmid, dim[j], acc2[4 * w + j]);
-            acc3[4 * w + j] = dp4a_us(wlo, dim[j], acc3[4 * w + j]);
+        for (int g = 0; g < 2; ++g) {
+          // a group without a token left weighs nothing, whatever the ring holds there
+          const unsigned char* vp = st + S::kHalf + g * S::kSubs * S::kPartBytes;
+          uint32_t vw[4][W];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) load_words<W>(vp + i * S::kRows * D, vw[i]);
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            // four rows of four dims, turned into four dims of four rows
+            const uint32_t y0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
+            const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
+            const uint32_t y2 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+            const uint32_t y3 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+            const uint32_t dim[4] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632),
+                                     __byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc1[4 * w + j] = dp4a_us(whi[g], dim[j], acc1[4 * w + j]);
+              acc2[4 * w + j] = dp4a_us(wmid[g], dim[j], acc2[4 * w + j]);
+              acc3[4 * w + j] = dp4a_us(wlo[g], dim[j], acc3[4 * w + j]);
+            }
           }
         }
       }
@@ -678,6 +703,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
     more = !aligned && find_item();
     if (more) {
       load_ids();
+      fetch_q();
       start_copies();
     }
 
@@ -691,6 +717,7 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
 #pragma unroll
       for (int j = 0; j < 4 * W; ++j) o[j] += __shfl_xor_sync(0xffffffffu, o[j], off);
     }
+    if (more) fetch_angles();
     if (by_warp) {
       float f = 1.f, fs = 0.f;
       if (a.k_self) {
@@ -813,8 +840,9 @@ __global__ void __launch_bounds__(kQ8Threads, kQ8BlocksPerSm) q8_decode_kernel(Q
   }
 }
 
-// For d > 1, with 2^k < d <= 2^(k + 1) and factor = ceil(2^(32 + k) / d), factor * d exceeds 2^(32 + k) by
-// less than 2^(k + 1), which is too little to carry a quotient of a < 2^31 to the next integer.
+// For d > 1, with 2^k < d <= 2^(k + 1) and factor = ceil(2^(32 + k) / d), factor * d exceeds
+// 2^(32 + k) by less than 2^(k + 1): too little to carry a quotient of a < 2^31 to the next
+// integer.
 Q8Divisor divisor(uint32_t d) {
   Q8Divisor r{0, 0};
   if (d == 1) return r;                     // factor 0: divides by one
@@ -823,7 +851,8 @@ Q8Divisor divisor(uint32_t d) {
   return r;
 }
 
-int q8_max_blocks() { return sm_count() * kQ8BlocksPerSm; }
+constexpr int kQ8MostBlocksPerSm = 3;
+int q8_max_blocks() { return sm_count() * kQ8MostBlocksPerSm; }
 
 template <typename T, int D>
 cudaError_t launch_decode_td(Q8DecodeArgs a, cudaStream_t s) {
@@ -835,7 +864,8 @@ cudaError_t launch_decode_td(Q8DecodeArgs a, cudaStream_t s) {
       (((long long)a.max_pages << a.shift) + S::kTile - 1) / S::kTile;
   // at most one block per kQ8MinTiles tiles of every item
   const long long per_item = std::max(1LL, (tiles + kQ8MinTiles - 1) / kQ8MinTiles);
-  const long long grid = std::min<long long>((long long)a.B * a.H * per_item, q8_max_blocks());
+  const long long grid = std::min<long long>((long long)a.B * a.H * per_item,
+                                              sm_count() * S::kBlocksPerSm);
   a.by_grid = divisor((uint32_t)grid);
   a.by_warps = divisor((uint32_t)grid * kQ8Warps);
   q8_decode_kernel<T, D><<<(unsigned)grid, kQ8Threads, S::kBytes, s>>>(a);
