@@ -501,9 +501,11 @@ size_t lla_q8_cache_bytes(const lla_cfg* cfg, int32_t n_pages, int32_t page);
  *                                 max(amax / 127, 1.25 scale) and the codes of the earlier
  *                                 tokens are rounded again; later rows are not touched
  *   code = round(value / scale), ties to even.
- * An amax of 1e-30 or less stores zeros.  NaN is stored as 0 and an infinity as the
- * largest code (amax looks at finite values), with LLA_STATUS_NONFINITE.  A page must
- * belong to one appended sequence only: written from two, its contents are unspecified.
+ * An amax of 1e-30 or less asks for a scale of 0, whose values read as zeros.  A scale found
+ * on a page that is below 7.8e-33 or not finite, which no append leaves, counts as 0: what the
+ * earlier tokens held reads as zeros.  NaN is stored as 0 and an infinity as the largest code
+ * (amax looks at finite values), with LLA_STATUS_NONFINITE.  A page must belong to one
+ * appended sequence only: written from two, its contents are unspecified.
  * Sequences whose tok_start or ctx_len do not fit (LLA_STATUS_CTX_RANGE) and pages
  * outside the cache (LLA_STATUS_PAGE_RANGE) are skipped.  B <= 65535.
  */

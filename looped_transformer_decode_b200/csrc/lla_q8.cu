@@ -78,6 +78,12 @@ __device__ __forceinline__ bool known_page(const Q8AppendArgs& a, int page, bool
   return false;
 }
 
+// A page's scale from an earlier append; anything else (damaged, or for values that count as
+// zero) is taken for 0, which also bounds what a value is divided by.
+__device__ __forceinline__ bool usable_scale(float s) {
+  return s >= kQ8Tiny / 128.f && s <= FLT_MAX;
+}
+
 // Scale of the page after the append, from the largest new value.
 __device__ __forceinline__ float grown_scale(float amax, float older) {
   const float asked = amax > kQ8Tiny ? __fdiv_rn(amax, 127.f) : 0.f;
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) q8_append_kernel(Q8AppendAr
       rotate_chunk<N>(load_turn<N>(a.rope + (size_t)pos * (a.rd / 2), rc), rc.split, v);
   };
   float older = un.off > 0 ? *scale : 0.f;
-  if (!(older > 0.f && older <= FLT_MAX)) older = 0.f;
+  if (!usable_scale(older)) older = 0.f;
   float amax = 0.f;
   bool strange = false;
 #pragma unroll 1
@@ -273,8 +279,9 @@ q8_append_prompts_kernel(Q8AppendArgs a, int units) {
       if (rc.rotary) turns[i] = load_turn<N>(a.rope + (size_t)pos * (a.rd / 2), rc);
     }
     const bool known = known_page(a, page, tell);
-    int8_t* codes = (is_k ? a.kc : a.vc) + (((long long)page * a.H + g0 * teams + team0) << a.shift) * a.d;
-    float* scale = (is_k ? a.ks : a.vs) + (long long)page * a.H + g0 * teams + team0;
+    const long long run = (long long)page * a.H + g0 * teams + team0;
+    int8_t* codes = (is_k ? a.kc : a.vc) + (run << a.shift) * a.d;
+    float* scale = (is_k ? a.ks : a.vs) + run;
 
     int stage = 0;
     for (int g = g0; g < g1 && known; ++g, parity ^= 1) {    // the same for all teams
@@ -282,7 +289,7 @@ q8_append_prompts_kernel(Q8AppendArgs a, int units) {
       const int live = mine_too ? rows : 0;
       fetch(g + kDepth - 1, stage == 0 ? kDepth - 1 : stage - 1);
       float older = un.off > 0 && mine_too ? *scale : 0.f;
-      if (!(older > 0.f && older <= FLT_MAX)) older = 0.f;
+      if (!usable_scale(older)) older = 0.f;
       __pipeline_wait_prior(kDepth - 1);
       float v[kPasses][N];
       float amax = 0.f;

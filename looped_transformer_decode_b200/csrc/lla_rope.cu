@@ -136,7 +136,8 @@ cudaError_t launch_rope_t(RopeApplyArgs a, cudaStream_t s) {
   a.groups = many ? (a.n_heads + kHeads - 1) / kHeads : a.n_heads;
   const int per_tok = a.groups * tpr;
   a.tok_block = per_tok < kRopeThreads ? kRopeThreads / per_tok : 1;
-  const int threads = per_tok < kRopeThreads ? (a.tok_block * per_tok + 31) / 32 * 32 : kRopeThreads;
+  const int threads =
+      per_tok < kRopeThreads ? (a.tok_block * per_tok + 31) / 32 * 32 : kRopeThreads;
   const dim3 grid((unsigned)((a.n_tok + a.tok_block - 1) / a.tok_block),
                   (per_tok + kRopeThreads - 1) / kRopeThreads);
   if (many) rope_apply_kernel<T, kHeads><<<grid, threads, 0, s>>>(a);

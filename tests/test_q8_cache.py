@@ -262,6 +262,75 @@ def test_append_matches_reference(dtype, page, d, d_rope, layout, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,page,d,d_rope,layout,dtype,old,new", [
+    # few tokens for many sequences, but several pages of one of them
+    (3, 16, 64, 0, "half", torch.float32, [5] * 20, [100] + [0] * 19),
+    (20, 32, 96, 32, "interleaved", torch.bfloat16, [5, 31, 0, 64] * 5, [3, 2, 33, 1] * 5),
+    # prompts of more heads than a block's: its share begins and ends inside pages
+    (40, 64, 128, 64, "interleaved", torch.bfloat16, [0, 70, 5], [700, 0, 900]),
+    (33, 128, 128, 0, "half", torch.float32, [130, 0], [300, 259]),
+    (128, 16, 32, 0, "half", torch.bfloat16, [1, 0, 7, 16], [40, 16, 0, 400]),
+    (1, 64, 96, 64, "half", torch.float32, [63, 0], [1, 2000])])
+def test_append_of_many_heads_and_uneven_lengths(H, page, d, d_rope, layout, dtype, old, new):
+    old, new = np.array(old), np.array(new)
+    g = np.random.default_rng(H + page)
+    cfg = cfg_of(H, d, d_rope)
+    after = old + new
+    bt, n_pages = layout_pages(g, after, page)
+    cache = random_cache(g, cfg, n_pages, page)
+    before = [t.cpu().numpy().astype(np.float64) for t in (cache.k, cache.k_scale, cache.v,
+                                                           cache.v_scale)]
+    start = np.concatenate([[0], np.cumsum(new)])
+    n = int(start[-1])
+    k, v = (torch.from_numpy(g.standard_normal((n, H, d)) * 1.5).to(dtype).cuda() for _ in "kv")
+    pos = np.concatenate([np.arange(o, o + m) for o, m in zip(old, new)]).astype(int)
+    table = lla.rope_table(cfg, int(after.max()) + 1)
+    lla.q8_append(cfg, table, cache, i32(after), i32(bt), i32(start), i32(pos), k, v, layout=layout)
+    x = P.rope_rows(k.double().cpu().numpy(), *rows_of(table, pos), layout)
+    check_append(before[0], before[1], cache.k, cache.k_scale, bt, after, start, x)
+    check_append(before[2], before[3], cache.v, cache.v_scale, bt, after, start,
+                 v.double().cpu().numpy())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [3, 40])
+def test_append_onto_a_scale_that_no_append_leaves(n):
+    """A scale of 1e-38 counts as zero: the earlier tokens read as zeros, the new ones as
+    themselves, or as zeros where they count as zero too."""
+    cfg, page = cfg_of(2, 64), 16
+    cache = lla.q8_cache_alloc(cfg, 4, page)
+    cache.k.fill_(100)
+    cache.v.fill_(-100)
+    cache.k_scale.fill_(1e-38)
+    cache.v_scale.fill_(1e-38)
+    x = torch.zeros((n, 2, 64), device="cuda")
+    x[:, 0], x[:, 1] = 1e-31, 0.5
+    lla.q8_append(cfg, None, cache, i32([5 + n]), i32([[2, 0, 3]]), i32([0, n]), None, x, x)
+    at = torch.arange(5 + n, device="cuda")
+    k, v = lla.q8_read(cfg, cache, torch.tensor([2, 0, 3], device="cuda")[at // page] * page + at % page)
+    want = torch.zeros((5 + n, 2, 64), dtype=torch.bfloat16, device="cuda")
+    want[5:, 1] = 0.5
+    assert torch.equal(k, want) and torch.equal(v, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,H,d", [(6001, 5, 96), (40003, 1, 64), (513, 128, 128)])
+def test_read_of_many_rows(n, H, d):
+    cfg, page = cfg_of(H, d), 16
+    g = np.random.default_rng(n)
+    cache = random_cache(g, cfg, 9, page)
+    slot = torch.from_numpy(g.integers(0, 9 * page, n)).cuda()
+    slot[n - 1] = slot[n // 2] = 9 * page
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, v = lla.q8_read(cfg, cache, slot, status=st)
+    ok = slot < 9 * page
+    p, r = slot[ok] // page, slot[ok] % page
+    assert int(st) == lla.STATUS_SLOT_RANGE and not k[~ok].any() and not v[~ok].any()
+    assert torch.equal(k[ok], (cache.k[p, :, r].float() * cache.k_scale[p][..., None]).bfloat16())
+    assert torch.equal(v[ok], (cache.v[p, :, r].float() * cache.v_scale[p][..., None]).bfloat16())
+
+
+@pytest.mark.gpu
 def test_token_by_token_append_stays_near_the_values():
     """A sequence grown one token at a time, values rising: each read value is within the
     geometric bound of its repeated roundings, 2.5 final scales."""
@@ -517,6 +586,8 @@ def test_decode_of_damaged_lists():
     out, st, _ = run([32, 40], [[0, 9], [1, 2]])      # a foreign page; longer than the table
     assert st == lla.STATUS_PAGE_RANGE | lla.STATUS_CTX_RANGE
     assert torch.allclose(out, want, atol=1e-6)       # the page left out, the length clamped
+    out, st, _ = run([32, 32], [[9, -1], [1, 2]])     # no page of a sequence there
+    assert st == lla.STATUS_PAGE_RANGE and torch.equal(out[0], q[0]) and torch.equal(out[1], want[1])
     out, st, _ = run([-3, 32], [[0, 3], [1, 2]])
     assert st == lla.STATUS_CTX_RANGE and torch.equal(out[0], q[0]) and torch.equal(out[1], want[1])
     out, st, _ = run([16, 32], [[0, 3], [1, 2]], pos=(-1, 4))

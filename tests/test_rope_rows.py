@@ -149,6 +149,42 @@ def test_rotated_rows_match_oracle(dtype, layout, d, d_rope, H, n, inverse):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 15, 17, 129])
+def test_scaled_table_of_few_positions(n):
+    got = lla.rope_table(cfg_of(96), n, scaling=lla.RopeScaling("linear", 3.0))
+    ang = np.arange(n)[:, None] * P.rope_angles(96, 10000.0, "linear", 3.0)
+    want = np.stack([np.cos(ang), np.sin(ang)], -1)
+    assert np.abs(got.double().cpu().numpy() - want).max() <= 2.0 ** -25 + n * 2.0 ** -50
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,layout,d,d_rope,H,n", [
+    (torch.bfloat16, "half", 96, 0, 7, 12001), (torch.float32, "interleaved", 128, 64, 5, 5003),
+    (torch.bfloat16, "interleaved", 32, 0, 1, 300001), (torch.float32, "half", 64, 32, 130, 301)])
+def test_many_rows_match_oracle(dtype, layout, d, d_rope, H, n):
+    """Calls large enough for a thread to take several heads, whose number is no multiple."""
+    cfg = cfg_of(d, d_rope, H=min(H, 128))
+    g = torch.Generator(device="cuda").manual_seed(n)
+    table = lla.rope_table(cfg, 900)
+    pos = torch.randint(0, 900, (n,), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn((n, H, d), generator=g, device="cuda").to(dtype)
+    got = lla.rope_apply(cfg, table, pos, x, layout=layout)
+    pick = torch.randint(0, n, (400,), generator=g, device="cuda")
+    pick[0], pick[1] = 0, n - 1
+    t = table.double()[pos[pick].long()].cpu().numpy()
+    xs = x[pick].double().cpu().numpy()
+    want = P.rope_rows(xs, t[..., 0], t[..., 1], layout, False)
+    err = np.abs(got[pick].double().cpu().numpy() - want)
+    assert (err <= pair_bound(xs, t, None, layout, want, dtype)).all()
+    # every row against the same rows in calls of a few, which a thread a head takes
+    few = torch.cat([lla.rope_apply(cfg, table, pos[i:i + 97], x[i:i + 97], layout=layout)
+                     for i in range(0, min(n, 970), 97)])
+    assert torch.equal(got[:few.shape[0]], few)
+    lla.rope_apply(cfg, table, pos, x, layout=layout, out=x)
+    assert torch.equal(x, got)
+
+
+@pytest.mark.gpu
 def test_strided_and_in_place_rows():
     """Slices of a fused projection, rows alternating in one buffer, and y = x."""
     cfg, n, H, d = cfg_of(64, H=4), 37, 4, 64
