@@ -26,7 +26,12 @@ constexpr float kQ8Grow = 1.25f;
 
 // ---------------------------------------------------------------- append
 
-constexpr int kAppendFew = 8;           // tokens per sequence
+// Tokens per sequence below which a warp per part is faster, and where there are many parts.
+// 8 sequences of 16 heads of 128: 4.3 us either way at 4 tokens, 8.3 against 5.3 by the kernel
+// for prompts at 16.  64 of them, in pages of 64: 4.1 against 7.9 at 1 token, 7.4 against 14.8
+// at 8, 11.3 against 17.5 at 16, 22.8 against 24.4 at 31.
+constexpr int kAppendFew = 8, kAppendFewOfMany = 24;
+constexpr int kAppendManyHeads = 512;   // of all sequences
 constexpr int kAppendWarps = 8;
 constexpr int kAppendBlocksPerSm = 2;
 constexpr int kAppendValues = 32;       // of a full page's head, per thread (prompts)
@@ -424,7 +429,8 @@ cudaError_t launch_append_prompts(Q8AppendArgs a, int units, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_append(Q8AppendArgs a, cudaStream_t s) {
   const int units = (a.n_tok >> a.shift) + 2 * a.B;
-  if (a.n_tok < kAppendFew * a.B) {
+  if (a.n_tok < kAppendFew * a.B ||
+      (a.n_tok < kAppendFewOfMany * a.B && a.B * a.H >= kAppendManyHeads)) {
     const int warps = std::min(kAppendWarps, 2 * a.H);
     const dim3 grid(units, (2 * a.H + warps - 1) / warps);
     q8_append_kernel<T><<<grid, 32 * warps, 0, s>>>(a);

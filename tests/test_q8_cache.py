@@ -266,6 +266,7 @@ def test_append_matches_reference(dtype, page, d, d_rope, layout, case):
     # few tokens for many sequences, but several pages of one of them
     (3, 16, 64, 0, "half", torch.float32, [5] * 20, [100] + [0] * 19),
     (20, 32, 96, 32, "interleaved", torch.bfloat16, [5, 31, 0, 64] * 5, [3, 2, 33, 1] * 5),
+    (40, 64, 64, 0, "half", torch.float32, [5, 31, 0, 64] * 5, [13, 2, 33, 10] * 5),
     # prompts of more heads than a block's: its share begins and ends inside pages
     (40, 64, 128, 64, "interleaved", torch.bfloat16, [0, 70, 5], [700, 0, 900]),
     (33, 128, 128, 0, "half", torch.float32, [130, 0], [300, 259]),
