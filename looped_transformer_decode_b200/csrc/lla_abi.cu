@@ -1,5 +1,6 @@
 // C ABI entry points: argument validation, exact bookkeeping, launch planning.
 // Every check runs on the host before anything is enqueued.
+#include <atomic>
 #include <cstdio>
 #include <cstdarg>
 #include <cstring>
@@ -152,15 +153,22 @@ PackedLayout packed_layout(const lla_cfg& c) {
   return L;
 }
 
+// Asked several times a call (workspace sizes, grids), so each device's count is kept.
 int sm_count() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-      sms <= 0) {
-    cudaGetLastError();   // a failed query leaves an error behind; clear it
-    return 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) {
+    if (dev >= 0 && dev < kDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0)
+      return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+        sms > 0) {
+      if (dev >= 0 && dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
+      return sms;
+    }
   }
-  return sms;
+  cudaGetLastError();   // a failed query leaves an error behind; clear it
+  return 148;
 }
 
 SplitPlan split_plan(const lla_cfg& c, int B, int n_cap) {
