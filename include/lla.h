@@ -414,7 +414,8 @@ int lla_rope_table_scaled(const lla_cfg* cfg, const lla_rope_scaling* scaling, i
  *   (y_a, y_b) = (x_a c - x_b s, x_a s + x_b c) on the pairs (a, b) of `layout` among the
  *   rotary dims, (c, s) the table's row at positions[token]; other dims are copied.
  * inverse != 0 rotates back, which is also the gradient: dL/dx = inverse rotation of dL/dy.
- *   x, y       device, dtype LLA_F32 or LLA_BF16 (arithmetic in fp32): token i's heads
+ *   x, y       device, dtype LLA_F32 or LLA_BF16 (arithmetic in fp32, each product and
+ *              each sum rounded): token i's heads
  *              start at element i * stride and are contiguous; strides in elements, whole
  *              multiples of 16 bytes, at least n_heads * d_head.  y == x with the same
  *              stride rotates in place; rows of x and y must not overlap otherwise
@@ -495,7 +496,9 @@ size_t lla_q8_cache_bytes(const lla_cfg* cfg, int32_t n_pages, int32_t page);
  *              elements apart (as lla_rope_apply's); n_tok rows are there to read.
  *   rope_table, rope_max_pos, layout, positions [n_tok]: keys are rotated in fp32 on the way,
  *              as by lla_rope_apply.  rope_table NULL: keys come rotated, positions unused.
- * Per page and head, with amax the largest magnitude among the new tokens' values:
+ * Per page and head, with amax the largest magnitude among the new tokens' values, in fp32
+ * (every product rounded; amax / 127 is amax * fp32(1 / 127), value / scale is
+ * value * fp32(1 / scale), so that codes repeat bit by bit from elementary operations):
  *   page without earlier tokens   scale = amax / 127
  *   page with earlier tokens      scale kept if amax / 127 <= scale, else it becomes
  *                                 max(amax / 127, 1.25 scale) and the codes of the earlier

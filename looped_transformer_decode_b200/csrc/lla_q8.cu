@@ -89,10 +89,12 @@ __device__ __forceinline__ bool usable_scale(float s) {
   return s >= kQ8Tiny / 128.f && s <= FLT_MAX;
 }
 
-// Scale of the page after the append, from the largest new value.
+// Scale of the page after the append, from the largest new value.  amax / 127 is a product with
+// the nearest 1 / 127, as in the definition: in bf16 a quotient value / scale often lies at half a
+// step, and one unit in the last place of the scale decides its code.
 __device__ __forceinline__ float grown_scale(float amax, float older) {
-  const float asked = amax > kQ8Tiny ? __fdiv_rn(amax, 127.f) : 0.f;
-  return asked > older ? fmaxf(asked, older * kQ8Grow) : older;
+  const float asked = amax > kQ8Tiny ? __fmul_rn(amax, 1.f / 127.f) : 0.f;
+  return asked > older ? fmaxf(asked, __fmul_rn(older, kQ8Grow)) : older;
 }
 
 // The codes of four values x with |x inv| < 2^22: adding 1.5 * 2^23 rounds to an integer and

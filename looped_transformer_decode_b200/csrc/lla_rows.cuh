@@ -115,23 +115,23 @@ __device__ __forceinline__ Turn<N> load_turn(const float2* table_row, const RowC
   return t;
 }
 
+// (a, b) turned by (c, s), every product rounded: fused into the sum, the two outputs would round
+// differently from elementary fp32 operations, and a code next to a half step with them.
+__device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+  a = x;
+}
+
 // Rotate a chunk of a head's rotary dims.
 template <int N>
 __device__ __forceinline__ void rotate_chunk(const Turn<N>& t, bool split, float* v) {
   if (split) {
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-      const float a = v[j], b = v[j + N / 2];
-      v[j] = a * t.c[j] - b * t.s[j];
-      v[j + N / 2] = a * t.s[j] + b * t.c[j];
-    }
+    for (int j = 0; j < N / 2; ++j) rotate_pair(v[j], v[j + N / 2], t.c[j], t.s[j]);
   } else {
 #pragma unroll
-    for (int j = 0; j < N / 2; ++j) {
-      const float a = v[2 * j], b = v[2 * j + 1];
-      v[2 * j] = a * t.c[j] - b * t.s[j];
-      v[2 * j + 1] = a * t.s[j] + b * t.c[j];
-    }
+    for (int j = 0; j < N / 2; ++j) rotate_pair(v[2 * j], v[2 * j + 1], t.c[j], t.s[j]);
   }
 }
 
