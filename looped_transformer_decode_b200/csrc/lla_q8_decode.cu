@@ -592,7 +592,9 @@ q8_decode_kernel(Q8DecodeArgs a) {
       const float ks1 = scale_of(a.ks, id1), vs1 = scale_of(a.vs, id1);
       id2 = checked(t + 2 * step, id2);
       const int id3 = part_id(t + 3 * step);
-      if (!sm100::mbar_wait(&bars[s], (seq / kQ8Stages) & 1u, abort_flag)) {
+      // Each lane looks at the barrier, the abort flag and the timer for itself: near a timeout
+      // they may differ, and what follows is the whole warp's.
+      if (!__all_sync(0xffffffffu, sm100::mbar_wait(&bars[s], (seq / kQ8Stages) & 1u, abort_flag))) {
         // copies already issued land before the block can end
         for (int k = 0; k < kQ8Stages && t + k * step < it.t1; ++k) {
           const unsigned long long w0 = sm100::global_timer_ns();
