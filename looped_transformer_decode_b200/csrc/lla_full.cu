@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(kFullThreads, FullShape<D>::kCtasPerSm)
 
       for (int k = 0; !aborted && k < r.ntiles; ++k, ++it) {
         const uint32_t stage = it % NST, ph = (it / NST) & 1u;
-        if (!mbar_wait(&full[stage], ph, abort_flag)) {
+        // a vote: near a timeout the lanes' own results may differ, and full-mask shuffles follow
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], ph, abort_flag))) {
           aborted = true;
           break;
         }
