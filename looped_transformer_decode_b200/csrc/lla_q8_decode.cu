@@ -1,15 +1,14 @@
 // Decode attention over the paged 8-bit cache (its layout and scales: lla_q8.cu).
 //
-// q8_decode_kernel<T, D>: HBM-bound (2 D bytes per token and head against 4 D
-// operations), so the codes never become floats one by one:
+// q8_decode_kernel<T, D>: HBM-bound (2 D bytes per token and head against 4 D operations):
 //   scores   q is split once per item into three 7-bit integers, q = qs (q1 2^14 + q2 2^7
 //            + q3), and the dot products of four codes are one instruction each, exact in
 //            int32 (dp4a); the page's scale multiplies the finished score.
-//   values   a token's weight times its page's value scale, relative to the largest so
-//            far, is a 24-bit integer; its three bytes, of four tokens each, meet the codes
-//            of four tokens and one dim in dp4a, exact in int32 until a new largest weight
-//            rescales the sum in fp32.
-// About 1.5 instructions per code instead of the five of convert-and-multiply.
+//   values   fp32: a code becomes a float by a byte permutation and half of a packed add, and
+//            meets its token's weight p * scale in half of a packed fma.  Weights as integers
+//            (dp4a on the codes) take half the instructions, but are fixed point: beside one
+//            heavy token, or a page of large values, whatever weighs 2^-24 of it is lost, while
+//            the softmax's sum still counts it.
 //
 // Work: the tokens of all (sequence, head) items, in tiles of 4 KB of keys, divided among
 // the blocks from the lengths on the device, so that uneven sequences and few long ones
@@ -35,9 +34,6 @@ constexpr int kQ8Stages = 2;
 constexpr int kQ8MinTiles = 8;              // tiles worth a block
 constexpr int kQ8ItemBlock = 12;            // start and merge of an item in tiles, for a block
 constexpr int kQ8ItemWarp = 4;              // and for a warp that has it to itself
-constexpr int kQ8FlushTiles = 4096;         // 2 * 4 * 255 * 128 per tile and dim stays below 2^31
-constexpr float kQ8Weight = 16777200.f;     // below 2^24 - 1 by more than a product's roundings
-constexpr float kQ8SmallRef = 1e-31f;       // least reference of the weights
 
 template <int D>
 struct Q8Shape {
@@ -45,9 +41,9 @@ struct Q8Shape {
   // four of them are a group, the unit of the arithmetic.  kSubs 16-token blocks, each in
   // one page, make a group; two groups make a tile.
   static constexpr int kLanes = D == 96 ? 8 : D / 16;
-  // Registers bound the blocks per SM.  Two take 250 a thread and hold both groups' values;
-  // three of 168 spill (256 sequences of 4096 tokens, 16 heads of 128: 644 us against 687) but
-  // for 96, whose lanes hold 12 codes.
+  // Registers bound the blocks per SM: two take 180 a thread, three of 168 fit without spills but
+  // divide middling batches worse (16 heads of 128; 64 x 512 tokens 30 us against 37, 256 x 4096
+  // 645 against 652, 1024 x 64 88 against 74).  Lanes of 96 hold 12 codes and need fewer.
   static constexpr int kBlocksPerSm = D == 96 ? 3 : 2;
   static constexpr int kWords = D / kLanes / 4;             // 4-code words per lane and row
   static constexpr int kRows = 32 / kLanes;
@@ -79,11 +75,39 @@ __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// sum of four products, unsigned bytes of a with signed bytes of b
-__device__ __forceinline__ int dp4a_us(uint32_t a, uint32_t b, int c) {
-  int d;
-  asm("dp4a.u32.s32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
+// Two floats in a register pair, and arithmetic on both, each rounded as by itself.
+typedef unsigned long long float_pair;
+__device__ __forceinline__ float_pair pair_of(float a, float b) {
+  float_pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(float_pair p, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ float_pair add2(float_pair a, float_pair b) {
+  float_pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float_pair mul2(float_pair a, float_pair b) {
+  float_pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float_pair fma2(float_pair a, float_pair b, float_pair c) {
+  float_pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// Codes j and j + 1 of a word whose sign bits are flipped, as floats: 2^23 + 128 + code has the
+// byte as its lowest mantissa bits.
+template <int J>
+__device__ __forceinline__ float_pair codes2(uint32_t flipped) {
+  const float lo = __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7440 + J));
+  const float hi = __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7441 + J));
+  return add2(pair_of(lo, hi), pair_of(-8388736.f, -8388736.f));
 }
 
 template <int W>
@@ -553,32 +577,12 @@ q8_decode_kernel(Q8DecodeArgs a) {
       }
     }
 
-    // Sums are relative to 2^m, m the largest score so far: l of 2^(s - m), o of
-    // 2^(s - m) v.  acc holds weights w = 2^(s - m) vs / R * kQ8Weight times codes, R
-    // the reference that no weight since the last flush exceeds.  A larger weight flushes
-    // acc into o; a larger score rescales l, o and R.
-    float m = -INFINITY, l = 0.f, R = 0.f, wf = 0.f;             // wf = kQ8Weight / R
-    float o[4 * W];
-    int acc1[4 * W], acc2[4 * W], acc3[4 * W];
+    // Sums are relative to 2^m, m the largest score so far: l of p = 2^(s - m), o of p * scale *
+    // code.  A larger score rescales both.
+    float m = -INFINITY, l = 0.f;
+    float_pair o2[2 * W];                                        // dims 2 j and 2 j + 1
 #pragma unroll
-    for (int j = 0; j < 4 * W; ++j) {
-      o[j] = 0.f;
-      acc1[j] = acc2[j] = acc3[j] = 0;
-    }
-    int since = 0;                                               // tiles since the last flush
-    bool held = false;                                           // acc holds something
-    auto flush = [&]() {
-      if (!held) return;
-      held = false;
-      const float f = R * (1.f / kQ8Weight);
-#pragma unroll
-      for (int j = 0; j < 4 * W; ++j) {
-        o[j] = fmaf(f, fmaf((float)acc1[j], 65536.f, fmaf((float)acc2[j], 256.f, (float)acc3[j])),
-                    o[j]);
-        acc1[j] = acc2[j] = acc3[j] = 0;
-      }
-      since = 0;
-    };
+    for (int j = 0; j < 2 * W; ++j) o2[j] = 0;
 
     // Rows r + kRows i of a group are a lane's, i = 0 .. 3; it ends up with the scores of
     // i_own (and i_own + 1 when it has two).
@@ -605,7 +609,6 @@ q8_decode_kernel(Q8DecodeArgs a) {
         aborted = true;
         break;
       }
-      if (++since >= kQ8FlushTiles) flush();
       const unsigned char* st = ring + s * S::kStage + r * D + col * 4 * W;
       const int rows_left = it.n - t * S::kTile - r - S::kRows * i_own;   // of a lane's first score
       if (live) {                                               // else no page of it is there
@@ -614,7 +617,7 @@ q8_decode_kernel(Q8DecodeArgs a) {
         constexpr int kFar = S::kLanes / 2, kNear = S::kLanes / 4;
         const bool upper = col & kFar, odd = col & kNear;
         float sc[2][S::kScores], vsc[2][S::kScores];
-        bool above = false, heavy = false;
+        bool above = false;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const unsigned char* kp = st + g * S::kSubs * S::kPartBytes;
@@ -650,7 +653,6 @@ q8_decode_kernel(Q8DecodeArgs a) {
             const bool there = rows_left > g * S::kGroup + k * S::kRows && (live >> sub & 1);
             sc[g][k] = there ? x[k] * ksc : -INFINITY;
             above |= sc[g][k] > m;
-            heavy |= vsc[g][k] > R;                               // weights are at most vs: p <= 1
           }
         }
         if (__any_sync(0xffffffffu, above)) {
@@ -660,52 +662,31 @@ q8_decode_kernel(Q8DecodeArgs a) {
           const float f = exp2_down(m - mt);                      // 0 the first time
           m = mt;
           l *= f;
-          R *= f;
+          const float_pair f2 = pair_of(f, f);
 #pragma unroll
-          for (int j = 0; j < 4 * W; ++j) o[j] *= f;
-          if (R < kQ8SmallRef) {                                  // 1 / R stays finite
-            flush();
-            R = kQ8SmallRef;
-          }
-          wf = kQ8Weight / R;
-          heavy = true;
+          for (int j = 0; j < 2 * W; ++j) o2[j] = mul2(o2[j], f2);
         }
-        if (__any_sync(0xffffffffu, heavy)) {
-          float top = fmaxf(fmaxf(vsc[0][0], vsc[0][S::kScores - 1]),
-                            fmaxf(vsc[1][0], vsc[1][S::kScores - 1]));
-          top = warp_largest(top);
-          if (top > R) {
-            flush();
-            R = top;
-            wf = kQ8Weight / R;
-          }
-        }
-        held = true;
-        uint32_t whi[2], wmid[2], wlo[2];     // bytes of the weights of a lane's four rows
+        float_pair weight[2][4];              // of a lane's four rows, twice
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          uint32_t wt[S::kScores];
+          float wt[S::kScores];
 #pragma unroll
           for (int k = 0; k < S::kScores; ++k) {
             const float p = exp2_down(sc[g][k] - m);
             l += p;
-            wt[k] = __float2uint_rn(p * (vsc[g][k] * wf));
+            wt[k] = p > 0.f ? p * vsc[g][k] : 0.f;                // a row past the end: whatever its scale
           }
-          uint32_t e0 = wt[0], e1 = wt[S::kScores - 1];
+          float e0 = wt[0], e1 = wt[S::kScores - 1];
           if constexpr (S::kLanes >= 4) {
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, wt[0], kNear);
+            const float other = __shfl_xor_sync(0xffffffffu, wt[0], kNear);
             e0 = odd ? other : wt[0];
             e1 = odd ? wt[0] : other;
           }
-          const uint32_t f0 = __shfl_xor_sync(0xffffffffu, e0, kFar);
-          const uint32_t f1 = __shfl_xor_sync(0xffffffffu, e1, kFar);
-          const uint32_t g0 = upper ? f0 : e0, g1 = upper ? f1 : e1;
-          const uint32_t g2 = upper ? e0 : f0, g3 = upper ? e1 : f1;
-          const uint32_t a01 = __byte_perm(g0, g1, 0x5140), a23 = __byte_perm(g2, g3, 0x5140);
-          const uint32_t h01 = __byte_perm(g0, g1, 0x0062), h23 = __byte_perm(g2, g3, 0x0062);
-          wlo[g] = __byte_perm(a01, a23, 0x5410);
-          wmid[g] = __byte_perm(a01, a23, 0x7632);
-          whi[g] = __byte_perm(h01, h23, 0x5410);
+          const float f0 = __shfl_xor_sync(0xffffffffu, e0, kFar);
+          const float f1 = __shfl_xor_sync(0xffffffffu, e1, kFar);
+          const float w4[4] = {upper ? f0 : e0, upper ? f1 : e1, upper ? e0 : f0, upper ? e1 : f1};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) weight[g][i] = pair_of(w4[i], w4[i]);
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -716,19 +697,17 @@ q8_decode_kernel(Q8DecodeArgs a) {
           for (int i = 0; i < 4; ++i) load_words<W>(vp + i * S::kRows * D, vw[i]);
 #pragma unroll
           for (int w = 0; w < W; ++w) {
-            // four rows of four dims, turned into four dims of four rows
-            const uint32_t y0 = __byte_perm(vw[0][w], vw[1][w], 0x5140);
-            const uint32_t y1 = __byte_perm(vw[2][w], vw[3][w], 0x5140);
-            const uint32_t y2 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-            const uint32_t y3 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-            const uint32_t dim[4] = {__byte_perm(y0, y1, 0x5410), __byte_perm(y0, y1, 0x7632),
-                                     __byte_perm(y2, y3, 0x5410), __byte_perm(y2, y3, 0x7632)};
+            // the four rows' sum by itself: long sums then take a quarter of the roundings
+            float_pair lo = 0, hi = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc1[4 * w + j] = dp4a_us(whi[g], dim[j], acc1[4 * w + j]);
-              acc2[4 * w + j] = dp4a_us(wmid[g], dim[j], acc2[4 * w + j]);
-              acc3[4 * w + j] = dp4a_us(wlo[g], dim[j], acc3[4 * w + j]);
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t u = vw[i][w] ^ 0x80808080u;
+              const float_pair c0 = codes2<0>(u), c2 = codes2<2>(u);
+              lo = i ? fma2(c0, weight[g][i], lo) : mul2(c0, weight[g][i]);
+              hi = i ? fma2(c2, weight[g][i], hi) : mul2(c2, weight[g][i]);
             }
+            o2[2 * w] = add2(o2[2 * w], lo);
+            o2[2 * w + 1] = add2(o2[2 * w + 1], hi);
           }
         }
       }
@@ -754,7 +733,9 @@ q8_decode_kernel(Q8DecodeArgs a) {
     }
 
     // ---------------------------------------------------------------- merge the warps
-    flush();
+    float o[4 * W];
+#pragma unroll
+    for (int j = 0; j < 2 * W; ++j) unpair(o2[j], o[2 * j], o[2 * j + 1]);
     if (S::kLanes == 8) l *= 0.5f;                              // two lanes held every score
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
