@@ -1,9 +1,12 @@
 // Decode attention over the paged 8-bit cache (its layout and scales: lla_q8.cu).
 //
 // q8_decode_kernel<T, D>: HBM-bound (2 D bytes per token and head against 4 D operations):
-//   scores   q is split once per item into three 7-bit integers, q = qs (q1 2^14 + q2 2^7
-//            + q3), and the dot products of four codes are one instruction each, exact in
-//            int32 (dp4a); the page's scale multiplies the finished score.
+//   scores   a lane's 16 dims of q (12 of 96) are split once per item into the three bytes of
+//            24-bit integers, q = qs (q1 2^16 + q2 2^8 + q3), and the dot products of four codes
+//            are one instruction each, exact in int32 (dp4a); a lane's sum meets its own qs, the
+//            finished score the page's scale.  Each element of q is held to 2^-24 of the largest
+//            of its 16: what fp32 sums with that element round away too, unless its keys are
+//            zero.  Four 7-bit integers of the whole head's largest element cost 5 %.
 //   values   fp32: a code becomes a float by a byte permutation and half of a packed add, and
 //            meets its token's weight p * scale in half of a packed fma.  Weights as integers
 //            (dp4a on the codes) take half the instructions, but are fixed point: beside one
@@ -43,7 +46,7 @@ struct Q8Shape {
   static constexpr int kLanes = D == 96 ? 8 : D / 16;
   // Registers bound the blocks per SM: two take 180 a thread, three of 168 fit without spills but
   // divide middling batches worse (16 heads of 128; 64 x 512 tokens 30 us against 37, 256 x 4096
-  // 645 against 652, 1024 x 64 88 against 74).  Lanes of 96 hold 12 codes and need fewer.
+  // 642 against 657, 1024 x 64 88 against 74).  Lanes of 96 hold 12 codes and need fewer.
   static constexpr int kBlocksPerSm = D == 96 ? 3 : 2;
   static constexpr int kWords = D / kLanes / 4;             // 4-code words per lane and row
   static constexpr int kRows = 32 / kLanes;
@@ -74,6 +77,13 @@ __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// sum of four products, signed bytes of a with unsigned bytes of b
+__device__ __forceinline__ int dp4a_su(uint32_t a, uint32_t b, int c) {
+  int d;
+  asm("dp4a.s32.u32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
 
 // Two floats in a register pair, and arithmetic on both, each rounded as by itself.
 typedef unsigned long long float_pair;
@@ -536,10 +546,10 @@ q8_decode_kernel(Q8DecodeArgs a) {
     self *= a.kappa;
     __syncwarp();
 
-    // q as three signed digits of 7 bits, the largest |q| at 127 * 2^14: a lane splits four
-    // dims and takes the words of its own through shared memory
+    // q as 24-bit integers, the largest |q| of a lane's dims near 2^23: a lane splits four dims
+    // and takes the words of its own through shared memory
     uint32_t q1[W], q2[W], q3[W];
-    float score_scale;
+    float score_scale;                                          // of the lane's part of a score
     bool strange = false;                                       // a NaN or an infinity in q
     {
       float v[4] = {0.f, 0.f, 0.f, 0.f}, amax = 0.f;
@@ -550,23 +560,29 @@ q8_decode_kernel(Q8DecodeArgs a) {
         strange |= !(fabsf(v[j]) <= FLT_MAX);
       }
       strange = __any_sync(0xffffffffu, strange);               // and the values are read
-      amax = warp_largest(amax);
-      constexpr float kTop = 127.f * 16384.f;
-      const float inv = amax > kQ8Tiny ? kTop / amax : 0.f;
-      score_scale = strange ? 0.f : a.kappa * amax / kTop;      // strange: pl becomes NaN below
-      uint32_t hi = 0, mid = 0, lo = 0;
+      if constexpr (W == 4) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      } else {
+        const float mine = amax;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int x = __float2int_rn(v[j] * inv), y = (x + 64) >> 7, z = (y + 64) >> 7;
-        lo |= (uint32_t)((x - (y << 7)) & 255) << (8 * j);      // -64 .. 63
-        mid |= (uint32_t)((y - (z << 7)) & 255) << (8 * j);
-        hi |= (uint32_t)(z & 255) << (8 * j);                   // -127 .. 127
+        for (int k = 0; k < W; ++k)
+          amax = fmaxf(amax, __shfl_sync(0xffffffffu, mine, lane / W * W + k));
       }
+      constexpr float kTop = 8388480.f;                         // a product's rounding below 2^23
+      const float inv = amax > kQ8Tiny ? kTop / amax : 0.f;
+      // in units of q1 2^8 + q2; strange: pl becomes NaN below
+      score_scale = strange ? 0.f : __shfl_sync(0xffffffffu, a.kappa * amax / (kTop / 256.f), col * W);
+      uint32_t x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = (uint32_t)__float2int_rn(v[j] * inv);
       uint32_t* words = reinterpret_cast<uint32_t*>(qs);
       if (lane < D / 4) {
-        words[lane] = hi;
-        words[D / 4 + lane] = mid;
-        words[D / 2 + lane] = lo;
+        const uint32_t y01 = __byte_perm(x[0], x[1], 0x5140), y23 = __byte_perm(x[2], x[3], 0x5140);
+        const uint32_t z01 = __byte_perm(x[0], x[1], 0x0062), z23 = __byte_perm(x[2], x[3], 0x0062);
+        words[lane] = __byte_perm(z01, z23, 0x5410);            // -128 .. 127
+        words[D / 4 + lane] = __byte_perm(y01, y23, 0x7632);    // 0 .. 255
+        words[D / 2 + lane] = __byte_perm(y01, y23, 0x5410);
       }
       __syncwarp();
 #pragma unroll
@@ -630,10 +646,10 @@ q8_decode_kernel(Q8DecodeArgs a) {
 #pragma unroll
             for (int w = 0; w < W; ++w) {
               s1 = __dp4a((int)kw[w], (int)q1[w], s1);
-              s2 = __dp4a((int)kw[w], (int)q2[w], s2);
-              s3 = __dp4a((int)kw[w], (int)q3[w], s3);
+              s2 = dp4a_su(kw[w], q2[w], s2);
+              s3 = dp4a_su(kw[w], q3[w], s3);
             }
-            part[i] = fmaf((float)(s1 * 128 + s2), 128.f, (float)s3);
+            part[i] = fmaf((float)s3, 1.f / 256.f, (float)(s1 * 256 + s2)) * score_scale;
           }
           // sums over a row's lanes, each exchange halving what a lane holds
           float x[2];
@@ -648,7 +664,7 @@ q8_decode_kernel(Q8DecodeArgs a) {
           for (int k = 0; k < S::kScores; ++k) {
             // the 16-token block of the group that the row lies in
             const int sub = g * S::kSubs + (S::kSubs == 1 ? 0 : S::kSubs == 2 ? i_own >> 1 : i_own + k);
-            const float ksc = __shfl_sync(0xffffffffu, ks0, sub) * score_scale;
+            const float ksc = __shfl_sync(0xffffffffu, ks0, sub);
             vsc[g][k] = __shfl_sync(0xffffffffu, vs0, sub);
             const bool there = rows_left > g * S::kGroup + k * S::kRows && (live >> sub & 1);
             sc[g][k] = there ? x[k] * ksc : -INFINITY;

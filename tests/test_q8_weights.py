@@ -2,10 +2,11 @@
 
 Tolerance, from the probabilities: with p the softmax, the output is off by at most
   sum_j p_j |v_j| * (2 ds + r 2^-24)
-ds being the largest error of a score (fp32 sums of d + 8 terms, the query held to 2^-21 of its
-largest element) and r the roundings of a token's contribution: one sum per 16 tokens, one rescale
-per 32, and 80 for the exponential, the products and the merges.  No term depends on values that
-have no weight, and nothing is lost beside a heavy token.
+ds being the largest error of a score (fp32 sums of d + 8 terms, each element of the query held to
+2^-24 of the largest of its 16 neighbours, of 12 in heads of 96) and r the roundings of a token's
+contribution: one sum per 16 tokens, one rescale per 32, and 80 for the exponential, the products
+and the merges.  No term depends on values that have no weight, and nothing is lost beside a heavy
+token.
 """
 from __future__ import annotations
 
@@ -14,8 +15,6 @@ import pytest
 import torch
 
 import looped_transformer_decode_b200 as lla
-
-QUERY = 2.0 ** -21      # of its largest element
 
 
 def attend(kc, vc, ks, vs, q, page, dtype=torch.float32, sm_scale=1.0):
@@ -40,8 +39,9 @@ def attend(kc, vc, ks, vs, q, page, dtype=torch.float32, sm_scale=1.0):
     s = k @ q * sm_scale
     p = np.exp(s - s.max())
     p /= p.sum()
-    ds = sm_scale * ((d + 8) * 2.0 ** -24 * (np.abs(k) @ np.abs(q)).max()
-                     + QUERY * np.abs(q).max() * np.abs(k).sum(1).max())
+    top = np.abs(q).reshape(-1, 12 if d == 96 else 16)
+    top = np.broadcast_to(top.max(1, keepdims=True), top.shape).reshape(d)
+    ds = sm_scale * 2.0 ** -24 * ((d + 8) * (np.abs(k) @ np.abs(q)).max() + (np.abs(k) @ top).max())
     r = n / 16 + n / 32 + 80
     want = p @ v
     tol = (p @ np.abs(v)) * (2 * ds + r * 2.0 ** -24) + torch.finfo(dtype).eps / 2 * np.abs(want)
@@ -110,3 +110,21 @@ def test_scores_that_rise_to_the_end_and_fall(d, page, dtype):
         q[0] = 30.0
         got, want, tol = attend(kc, vc, ks, vs, q, page, dtype)
         assert (np.abs(got - want) <= tol).all(), np.abs((got - want) / tol).max()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,page,dtype", [(128, 16, torch.float32), (96, 64, torch.float32),
+                                          (64, 32, torch.bfloat16), (32, 128, torch.float32)])
+@pytest.mark.parametrize("outlier", [30.0, 1e4, -1e7])
+def test_a_query_with_an_outlier(d, page, dtype, outlier):
+    """One element far above the rest, among 16 (or 12) dims where the keys are zero: the other
+    dims decide, and keep all their bits."""
+    n, group = 1000, 12 if d == 96 else 16
+    g = np.random.default_rng(d)
+    kc, vc = codes_of(g, (n, d)), codes_of(g, (n, d))
+    kc[:, group:2 * group] = 0
+    ks, vs = np.full(-(-n // page), 1 / 36), np.full(-(-n // page), 1 / 36)
+    q = g.standard_normal(d)
+    q[group + 3] = outlier
+    got, want, tol = attend(kc, vc, ks, vs, q, page, dtype, sm_scale=0.25)
+    assert (np.abs(got - want) <= tol).all(), np.abs((got - want) / tol).max()
