@@ -450,7 +450,8 @@ int lla_rope_apply(const lla_cfg* cfg, const void* rope_table, int32_t rope_max_
  *              index in its sequence; 0 past the last token.
  * Pages given back are free for the same call.  Growing sequences are served in order:
  * one whose pages, with all that was asked before it, exceed the free ones, or whose
- * tokens likewise exceed tok_cap, is left as it was (LLA_STATUS_PAGES_SHORT), and so is
+ * tokens likewise exceed tok_cap, is left as it was (LLA_STATUS_PAGES_SHORT; the tokens after
+ * it move up in tok_start, see row_start at lla_q8_append_rows), and so is
  * one that would pass max_pages * page tokens or whose ctx_len is outside that range
  * (LLA_STATUS_CTX_RANGE).  Dropping the tokens a call just appended restores free_list,
  * n_free, ctx_len and block_table (whose new entries become -1).  A page index outside
@@ -490,8 +491,10 @@ typedef struct lla_q8_cache {
 size_t lla_q8_cache_bytes(const lla_cfg* cfg, int32_t n_pages, int32_t page);
 
 /*
- * Append tokens: tokens tok_start[b] .. tok_start[b + 1] of k and v are the last ones of
- * sequence b, whose length with them is ctx_len[b] (as lla_page_map leaves them).
+ * Append tokens: rows tok_start[b] .. tok_start[b + 1] of k and v are the last tokens of
+ * sequence b, whose length with them is ctx_len[b] (as lla_page_map leaves them).  A sequence
+ * that lla_page_map refused has no rows there: where k and v hold some all the same, call
+ * lla_q8_append_rows.
  *   k, v       dtype LLA_F32 or LLA_BF16, rows of H heads of d_head, k_stride / v_stride
  *              elements apart (as lla_rope_apply's); n_tok rows are there to read.
  *   rope_table, rope_max_pos, layout, positions [n_tok]: keys are rotated in fp32 on the way,
@@ -510,7 +513,8 @@ size_t lla_q8_cache_bytes(const lla_cfg* cfg, int32_t n_pages, int32_t page);
  * (amax looks at finite values), with LLA_STATUS_NONFINITE.  A page must belong to one
  * appended sequence only: written from two, its contents are unspecified.
  * Sequences whose tok_start or ctx_len do not fit (LLA_STATUS_CTX_RANGE) and pages
- * outside the cache (LLA_STATUS_PAGE_RANGE) are skipped.  B <= 65535.
+ * outside the cache (LLA_STATUS_PAGE_RANGE) are skipped.  B <= 65535.  With no token, page or
+ * table entry at all (B, n_tok, n_pages or max_pages 0) nothing is enqueued and no bit set.
  */
 int lla_q8_append(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
                   int32_t rope_max_pos, int32_t layout, int32_t dtype, int32_t B,
@@ -518,6 +522,22 @@ int lla_q8_append(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rop
                   int32_t n_tok, const int32_t* tok_start, const int32_t* positions,
                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                   int32_t* status, void* stream);
+
+/*
+ * lla_q8_append for k and v whose rows were laid out before the call that grew the sequences:
+ * sequence b's tokens are rows row_start[b], row_start[b] + 1, ... of k and v (device int32 [B];
+ * 0, 1, .. B - 1 for a decode step with a row per sequence).  lla_page_map packs tok_start over
+ * the sequences that it served, so after a refusal (or beside a sequence that did not grow) token
+ * tok_start[b] is no longer row tok_start[b]: without row_start every later sequence would store
+ * another one's keys and values.  A sequence whose rows do not lie within the n_tok rows is
+ * skipped (LLA_STATUS_CTX_RANGE).  positions stay in the order of tok_start.
+ */
+int lla_q8_append_rows(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
+                       int32_t rope_max_pos, int32_t layout, int32_t dtype, int32_t B,
+                       int32_t max_pages, const int32_t* ctx_len, const int32_t* block_table,
+                       int32_t n_tok, const int32_t* tok_start, const int32_t* positions,
+                       const int32_t* row_start, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, int32_t* status, void* stream);
 
 /*
  * Rows of the cache as bf16: k_out, v_out [n_rows][H][d_head] = code * scale of row slot[i]

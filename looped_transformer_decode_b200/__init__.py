@@ -293,7 +293,8 @@ def page_map(page: int, ctx_len, n_new, block_table, free_list, n_free, tok_cap:
 
     Updates ``ctx_len`` [B], ``block_table`` [B, max_pages], ``free_list`` [n_pages] and
     ``n_free`` [1] (all int32) in place.  Returns (tok_start int32 [B + 1], slot int64 [tok_cap],
-    positions int32 [tok_cap]) of the appended tokens.
+    positions int32 [tok_cap]) of the appended tokens.  A sequence that finds no page is left as it
+    was and has none of them (``STATUS_PAGES_SHORT``); see ``row_start`` of ``q8_append``.
     """
     return _binding.page_map(page, ctx_len, n_new, block_table, free_list, n_free, tok_cap,
                              tok_start, slot, positions, status)
@@ -328,15 +329,19 @@ def q8_cache_alloc(cfg: Cfg, n_pages: int, page: int, device="cuda") -> Q8Cache:
 
 
 def q8_append(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, tok_start, positions, k, v,
-              layout: str = "half", status=None):
+              layout: str = "half", status=None, row_start=None):
     """Quantise new tokens' keys and values into the cache's pages (see ``lla_q8_append``).
 
     ``k``, ``v`` fp32 or bf16 [n_tok, H, d], tokens possibly strided; ``ctx_len`` and
     ``tok_start`` as ``page_map`` leaves them.  Keys are rotated by ``rope`` at ``positions`` int32
     [n_tok]; with ``rope=None`` (then ``positions`` may be None) they come rotated.
+
+    Token i is row i of ``k`` and ``v``.  ``page_map`` leaves sequences that it refuses out of
+    ``tok_start``, so where the rows were made for every sequence before it was known which grow (a
+    decode step), give ``row_start`` int32 [B], the first row of each sequence: ``arange(B)`` there.
     """
     _binding.q8_append(cfg, rope, cache, ctx_len, block_table, tok_start, positions, k, v, layout,
-                       status)
+                       status, row_start)
 
 
 def q8_read(cfg: Cfg, cache: Q8Cache, slot, k_out=None, v_out=None, status=None):

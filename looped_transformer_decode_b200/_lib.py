@@ -142,6 +142,8 @@ SIGNATURES = {
     "lla_q8_cache_bytes": (_SZ, [_CFG, _I32, _I32]),
     "lla_q8_append": (ctypes.c_int, [_CFG, _Q8, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32, _P,
                                      _P, _P, _I64, _P, _I64, _P, _P]),
+    "lla_q8_append_rows": (ctypes.c_int, [_CFG, _Q8, _P, _I32, _I32, _I32, _I32, _I32, _P, _P, _I32,
+                                          _P, _P, _P, _P, _I64, _P, _I64, _P, _P]),
     "lla_q8_read": (ctypes.c_int, [_CFG, _Q8, _I64, _P, _P, _P, _P, _P]),
     "lla_q8_decode_workspace_bytes": (_SZ, [_CFG, _I32, _I32]),
     "lla_q8_decode_launches": (ctypes.c_int, [_CFG, _I32, _I32]),

@@ -327,10 +327,10 @@ PyObject* page_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (cfg, rope, cache, ctx_len, block_table, tok_start, positions, k, v, layout, status)
+// (cfg, rope, cache, ctx_len, block_table, tok_start, positions, k, v, layout, status, row_start)
 PyObject* q8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  expect(n, 11);
+  expect(n, 12);
   const lla_cfg cfg = config(a[0]);
   const at::Tensor& k = leading(a[7], "k");
   const int kind = row_type(k, "k");
@@ -345,10 +345,13 @@ PyObject* q8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Rows kr = rows(a[7], type, dev, "k", shape), vr = rows(a[8], type, dev, "v", shape);
   const int32_t* positions =
       a[6] == Py_None ? nullptr : ints(a[6], dev, "positions", {tokens});
-  check(lla_q8_append(&cfg, &cache, table.p, table.positions, layout_of(a[9]), kind, bt.B,
-                      bt.max_pages, ints(a[3], dev, "ctx_len", {bt.B}), bt.p,
-                      small(tokens, "k"), ints(a[5], dev, "tok_start", {bt.B + 1}), positions,
-                      kr.p, kr.stride, vr.p, vr.stride, status_of(a[10], dev), stream_of(dev)));
+  const int32_t* row_start =
+      a[11] == Py_None ? nullptr : ints(a[11], dev, "row_start", {bt.B});
+  check(lla_q8_append_rows(&cfg, &cache, table.p, table.positions, layout_of(a[9]), kind, bt.B,
+                           bt.max_pages, ints(a[3], dev, "ctx_len", {bt.B}), bt.p,
+                           small(tokens, "k"), ints(a[5], dev, "tok_start", {bt.B + 1}), positions,
+                           row_start, kr.p, kr.stride, vr.p, vr.stride, status_of(a[10], dev),
+                           stream_of(dev)));
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

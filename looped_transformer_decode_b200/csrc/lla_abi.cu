@@ -765,6 +765,17 @@ int lla_q8_append(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rop
                   int32_t n_tok, const int32_t* tok_start, const int32_t* positions,
                   const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                   int32_t* status, void* stream) {
+  return lla_q8_append_rows(cfg, cache, rope_table, rope_max_pos, layout, dtype, B, max_pages,
+                            ctx_len, block_table, n_tok, tok_start, positions, nullptr, k, k_stride,
+                            v, v_stride, status, stream);
+}
+
+int lla_q8_append_rows(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
+                       int32_t rope_max_pos, int32_t layout, int32_t dtype, int32_t B,
+                       int32_t max_pages, const int32_t* ctx_len, const int32_t* block_table,
+                       int32_t n_tok, const int32_t* tok_start, const int32_t* positions,
+                       const int32_t* row_start, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, int32_t* status, void* stream) {
   int e = check_cfg(cfg);
   if (e) return e;
   e = check_q8("lla_q8_append", cache);
@@ -779,7 +790,8 @@ int lla_q8_append(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rop
   if (!ctx_len || !block_table || !tok_start || !k || !v || (rope_table && !positions))
     return fail(LLA_ERR_INVALID, "lla_q8_append: NULL pointer argument");
   if (!aligned16(rope_table) || !aligned16(k) || !aligned16(v) || !aligned4(ctx_len) ||
-      !aligned4(block_table) || !aligned4(tok_start) || !aligned4(positions) || !aligned4(status))
+      !aligned4(block_table) || !aligned4(tok_start) || !aligned4(positions) ||
+      !aligned4(row_start) || !aligned4(status))
     return fail(LLA_ERR_INVALID, "lla_q8_append: misaligned pointer");
   const int64_t row = (int64_t)cfg->H * cfg->d_head;
   const int size = dtype == LLA_BF16 ? 2 : 4;
@@ -806,6 +818,7 @@ int lla_q8_append(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rop
   a.block_table = block_table;
   a.tok_start = tok_start;
   a.positions = positions;
+  a.row_start = row_start;
   a.k = k;
   a.v = v;
   a.k_stride = k_stride;

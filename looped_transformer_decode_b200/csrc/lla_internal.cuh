@@ -217,6 +217,7 @@ struct Q8AppendArgs {
   const int32_t* block_table;
   const int32_t* tok_start;
   const int32_t* positions;
+  const int32_t* row_start;        // first row of each sequence's tokens; null: tok_start
   const void* k;
   const void* v;
   long long k_stride, v_stride;

@@ -42,7 +42,7 @@ constexpr int kAppendDepth = 2;         // groups in the ring: one in work, the 
 struct AppendUnit {
   const int32_t* entry;       // of the page, in the block table
   int off, count;             // rows [off, off + count) of the page are new
-  int tok;                    // first of their tokens
+  int tok, row;               // first of their tokens, and its row of k and v
 };
 
 // All threads of the block look for the sequence together, blockDim.x starts at a time.
@@ -65,6 +65,11 @@ __device__ __forceinline__ bool append_unit(const Q8AppendArgs& a, int u, bool t
     if (tell && a.status) atomicOr(a.status, LLA_STATUS_CTX_RANGE);
     return false;
   }
+  const int first_row = a.row_start ? __ldg(a.row_start + lo) : s;
+  if (first_row < 0 || first_row > a.n_tok - (e - s)) {
+    if (tell && a.status) atomicOr(a.status, LLA_STATUS_CTX_RANGE);
+    return false;
+  }
   const int before = after - (e - s);
   const int j = u - ((s >> a.shift) + 2 * lo);
   const long long page_at = (long long)(before >> a.shift) + j;
@@ -74,6 +79,7 @@ __device__ __forceinline__ bool append_unit(const Q8AppendArgs& a, int u, bool t
   r.off = before > p0 ? (int)(before - p0) : 0;
   r.count = (int)(after - p0 < P ? after - p0 : P) - r.off;
   r.tok = s + (int)(p0 + r.off - before);
+  r.row = first_row + (r.tok - s);
   return true;
 }
 
@@ -171,7 +177,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) q8_append_kernel(Q8AppendAr
   const bool turn = is_k && a.rope;
   const RowChunk rc = row_chunk<N>(c, a.d, turn ? a.rd : 0, a.layout);
   const long long stride = is_k ? a.k_stride : a.v_stride;
-  const T* src = static_cast<const T*>(is_k ? a.k : a.v) + un.tok * stride + h * a.d;
+  const T* src = static_cast<const T*>(is_k ? a.k : a.v) + un.row * stride + h * a.d;
   const long long run = (long long)page * a.H + h;
   int8_t* codes = (is_k ? a.kc : a.vc) + (run << a.shift) * a.d;
   float* scale = (is_k ? a.ks : a.vs) + run;
@@ -262,7 +268,7 @@ q8_append_prompts_kernel(Q8AppendArgs a, int units) {
     const bool turn = is_k && a.rope;
     const RowChunk rc = row_chunk<N>(c, a.d, turn ? a.rd : 0, a.layout);
     const long long stride = is_k ? a.k_stride : a.v_stride, pass = rpp * stride;
-    const T* first = static_cast<const T*>(is_k ? a.k : a.v) + (un.tok + row0) * stride + rc.lo;
+    const T* first = static_cast<const T*>(is_k ? a.k : a.v) + (un.row + row0) * stride + rc.lo;
     auto fetch = [&](int g, int stage) {
       const int h = g * teams + team0;
       const T* row = first + h * a.d;
