@@ -67,6 +67,7 @@ extern "C" {
 #define LLA_STATUS_PAGE_RANGE 16    /* a page outside [0, n_pages), or a free list out of bounds */
 #define LLA_STATUS_PAGES_SHORT 32   /* lla_page_map: a sequence was not served */
 #define LLA_STATUS_NONFINITE 64     /* lla_q8_append: a NaN or an infinity among keys or values */
+#define LLA_STATUS_ROPE_TABLE 128   /* lla_decode_attn: a table of scaled frequencies; output invalid */
 
 /*
  * Codec geometry of one shared layer.
@@ -205,7 +206,8 @@ size_t lla_decode_workspace_bytes(const lla_cfg* cfg, int32_t B, int32_t n_cap);
  * (values are summed in latent space and up-projected once; equal to rebuilding
  * each V because the weights are linear in the rebuilt values.)
  *   packed        codec from lla_codec_pack (device)
- *   rope_table    table from lla_rope_table covering [0, rope_max_pos) (device)
+ *   rope_table    table from lla_rope_table covering [0, rope_max_pos) (device); one from
+ *                 lla_rope_table_scaled sets LLA_STATUS_ROPE_TABLE
  *   t             loop index, 0 <= t < T
  *   B, n_cap      batch and cache capacity per sequence (n_cap >= 0)
  *   ctx_len       device int32 [B]: history length of each sequence (<= n_cap)
@@ -404,7 +406,11 @@ typedef struct lla_rope_scaling {
 /*
  * lla_rope_table with scaled frequencies (same layout, size and accuracy).  Such a
  * table serves lla_rope_apply, the lla_q8_* and the lla_full_* calls, which take their
- * angles from it.  lla_decode_attn does not: its kernels form angles from rope_base.
+ * angles from it.  lla_decode_attn does not: its kernels form the history's angles from
+ * rope_base, and a scaled table would turn only the query by other ones.  So a table whose
+ * frequencies differ (kind not NONE, factor not 1) has a sine of -0 at position 0 of pair 0,
+ * which changes no rotation, and lla_decode_attn sets LLA_STATUS_ROPE_TABLE for it.  (NTK alone
+ * can be had there: rope_base times s^(rd/(rd-2)).)
  */
 int lla_rope_table_scaled(const lla_cfg* cfg, const lla_rope_scaling* scaling, int32_t max_pos,
                           void* table, size_t table_bytes, void* stream);

@@ -15,7 +15,7 @@ import torch
 from ._lib import (BF16, ERR_CUDA, ERR_INVALID, ERR_TOO_SMALL, ERR_UNSUPPORTED, F32, LIB_PATH,
                    MODE_2D, MODE_PER_HEAD, OK, ROPE_LAYOUTS, SIGNATURES, STATUS_CTX_RANGE,
                    STATUS_NONFINITE, STATUS_PAGE_RANGE, STATUS_PAGES_SHORT, STATUS_POSITION_RANGE,
-                   STATUS_SLOT_RANGE, STATUS_TIMEOUT, Cfg, CQ8Cache, LLAError, RopeScaling, check,
+                   STATUS_ROPE_TABLE, STATUS_SLOT_RANGE, STATUS_TIMEOUT, Cfg, CQ8Cache, LLAError, RopeScaling, check,
                    last_error, lib)
 
 try:
@@ -33,7 +33,7 @@ __all__ = [
     "full_decode_workspace", "full_decode_launches", "full_decode_attn",
     "RopeScaling", "rope_apply", "page_map", "Q8Cache", "q8_cache_alloc", "q8_append", "q8_read",
     "q8_decode_workspace", "q8_decode_launches", "q8_decode_attn", "STATUS_TIMEOUT",
-    "STATUS_PAGE_RANGE", "STATUS_PAGES_SHORT", "STATUS_NONFINITE",
+    "STATUS_PAGE_RANGE", "STATUS_PAGES_SHORT", "STATUS_NONFINITE", "STATUS_ROPE_TABLE",
 ]
 
 
@@ -95,11 +95,14 @@ def codec_pack(cfg: Cfg, W_down_k, W_down_v, W_up_k, W_up_v, mu_k, mu_v, out=Non
 
 def rope_table(cfg: Cfg, max_pos: int, device="cuda", out=None, scaling: RopeScaling | None = None):
     """(cos, sin) rows [max_pos, rd / 2, 2].  ``scaling`` stretches the context (for rope_apply,
-    the q8 and the full-memory calls; decode_attn forms its angles from ``rope_base``)."""
+    the q8 and the full-memory calls; decode_attn forms its angles from ``rope_base`` and refuses
+    such a table, a copy of one by STATUS_ROPE_TABLE)."""
     c = cfg.c()
     if out is None:
         rd = cfg.d_rope or cfg.d_head                 # rotary dims
         out = torch.empty((max_pos, rd // 2, 2), dtype=torch.float32, device=device)
+    out.scaled_frequencies = (scaling is not None and scaling.kind != "none"
+                              and scaling.factor != 1)
     if scaling is not None:
         with torch.cuda.device(out.device):
             check(lib.lla_rope_table_scaled(cfg.ref, ctypes.byref(scaling.c()), max_pos,
@@ -160,6 +163,10 @@ def decode_attn(cfg: Cfg, packed, rope, t: int, ctx_len, q, k_self, v_self, posi
     n_cap = positions.shape[1]
     if H != cfg.H or d != cfg.d_head:
         raise ValueError("q shape does not match cfg")
+    for table in (rope, rope._base):
+        if getattr(table, "scaled_frequencies", False):
+            raise ValueError("rope has scaled frequencies: decode_attn forms the history's angles "
+                             "from cfg.rope_base")
     if out is None:
         out = torch.empty((B, H, d), dtype=torch.float32, device=q.device)
     if ws is None:

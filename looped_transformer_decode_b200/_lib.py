@@ -24,6 +24,7 @@ STATUS_TIMEOUT = 8
 STATUS_PAGE_RANGE = 16
 STATUS_PAGES_SHORT = 32
 STATUS_NONFINITE = 64
+STATUS_ROPE_TABLE = 128
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}

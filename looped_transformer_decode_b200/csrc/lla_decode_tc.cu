@@ -364,8 +364,10 @@ __global__ void __launch_bounds__(128) decode_prep_kernel(
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   // the CTA counter of the fused-combine kernels starts every call at zero (this
   // kernel runs first)
-  if (counters && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0)
-    counters[(size_t)gridDim.y * H] = 0u;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) {
+    if (counters) counters[(size_t)gridDim.y * H] = 0u;
+    if (scaled_table(rope)) atomicOr(status, LLA_STATUS_ROPE_TABLE);
+  }
   // This thread's first image chunk and first bias chunk need nothing from the query:
   // their W_up,k and mu values are read before the query's RoPE factors (which wait
   // for q_pos), so the two reads overlap.
@@ -1773,8 +1775,10 @@ __global__ void __launch_bounds__(128) decode_prep_f_kernel(
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
   const int lane = tid & 31, warp = tid >> 5;
   const int g = h % G;
-  if (counters && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
-    counters[(size_t)gridDim.y * H] = 0u;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
+    if (counters) counters[(size_t)gridDim.y * H] = 0u;
+    if (scaled_table(rope)) atomicOr(status, LLA_STATUS_ROPE_TABLE);
+  }
 
   // ---- reads that depend on nothing else
   const int qp_raw = q_pos[b];

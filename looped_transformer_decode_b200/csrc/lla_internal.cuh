@@ -174,6 +174,12 @@ cudaError_t launch_full_decode(const FullDecodeParams& p, const void* k_full, co
                                int grid, cudaStream_t s);
 
 // Rotary positions (lla_rope.cu).
+// Entry (position 0, pair 0) of a table of scaled frequencies: its sine is -0, which decode over
+// latents looks for.
+__device__ __forceinline__ bool scaled_table(const float2* rope) {
+  return __float_as_uint(__ldg(&rope[0].y)) == 0x80000000u;
+}
+
 struct RopeApplyArgs {
   const float2* rope;              // [rope_max_pos][rd/2]
   int rope_max_pos, d, rd, layout, n_heads, bf16;

@@ -257,6 +257,10 @@ __global__ void __launch_bounds__(128) decode_partial_kernel(DecodeArgs a) {
     qp = 0;
   }
 
+  // these kernels take every angle from the table, the tensor-core ones do not: refused alike
+  if (split == 0 && h == 0 && b == 0 && tid == 0 && scaled_table(a.rope))
+    atomicOr(a.status, LLA_STATUS_ROPE_TABLE);
+
   // Rotated query as complex pairs.
   const float* qh = a.q + ((size_t)b * a.H + h) * a.d;
   for (int i = tid; i < half; i += blockDim.x) {

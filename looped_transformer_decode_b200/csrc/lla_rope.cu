@@ -20,6 +20,7 @@ namespace {
 // and rounded once, so that far positions keep fp32 accuracy.
 struct RopeScale {
   int kind;
+  bool marked;             // frequencies differ from the plain ones: the table says so
   double base, factor, low, span;   // yarn: the ramp over i starts at low, is span wide
 };
 
@@ -68,6 +69,7 @@ rope_table_scaled_kernel(int max_pos, int half, RopeScale sc, float2* table) {
     s = c * t.y + s * t.x;
     c = x;
   }
+  if (sc.marked && pos0 == 0 && i == 0) table[0].y = -0.f;      // see scaled_table
 }
 
 // A thread rotates its chunk of kHeads heads of one token, 32 bytes of each in two 16-byte
@@ -152,6 +154,7 @@ cudaError_t launch_rope_table_scaled(const lla_cfg& c, const lla_rope_scaling& s
   const int rd = rotary_dims(c);
   RopeScale k{};
   k.kind = sc.kind;
+  k.marked = sc.kind != LLA_ROPE_SCALE_NONE && sc.factor != 1.0;
   k.base = (double)c.rope_base;
   k.factor = sc.factor;
   if (sc.kind == LLA_ROPE_SCALE_NTK) k.base = k.base * std::pow(sc.factor, rd / (rd - 2.0));
