@@ -684,8 +684,9 @@ int lla_rope_apply(const lla_cfg* cfg, const void* rope_table, int32_t rope_max_
   const uint64_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y);
   const bool apart = xa + xb <= ya || ya + yb <= xa;
   if (!apart && !(xa == ya && (x_stride == y_stride || n_tok == 1))) {
+    // a single row may have any stride, 0 too; it overlaps whatever is not apart from it
     const uint64_t st = (uint64_t)x_stride * size, rb = (uint64_t)row * size;
-    const uint64_t by = (xa > ya ? xa - ya : ya - xa) % st;
+    const uint64_t by = n_tok > 1 ? (xa > ya ? xa - ya : ya - xa) % st : 0;
     if (x_stride != y_stride || by < rb || st - by < rb)
       return fail(LLA_ERR_INVALID, "lla_rope_apply: rows of x and y overlap");
   }
