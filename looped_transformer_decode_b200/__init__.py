@@ -20,10 +20,19 @@ from ._lib import (BF16, ERR_CUDA, ERR_INVALID, ERR_TOO_SMALL, ERR_UNSUPPORTED, 
 
 try:
     from . import _binding          # needs torch and liblla.so loaded
+    _binding.set_error(LLAError)
 except ImportError as e:
-    raise ImportError(f"{e}: build the binding with `python -c \"import __graft_entry__ as g; "
-                      "g.build()\"`") from e
-_binding.set_error(LLAError)
+    class _Missing:
+        """The C++ binding could not be loaded: the calls that go through it say why."""
+
+        def __init__(self, why):
+            self.why = why
+
+        def __getattr__(self, name):
+            raise ImportError(f"{name} needs the package's C++ binding, and {self.why}: build it with "
+                              "`python -c \"import __graft_entry__ as g; g.build()\"`")
+
+    _binding = _Missing(str(e))
 
 __all__ = [
     "Cfg", "LLAError", "MODE_PER_HEAD", "MODE_2D", "ratio", "cache_bytes", "codec_pack",

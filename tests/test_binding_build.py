@@ -1,0 +1,48 @@
+"""The package without its C++ binding, and when the build makes the binding anew."""
+from __future__ import annotations
+
+import os
+import shutil
+import subprocess
+import sys
+
+import looped_transformer_decode_b200 as lla
+
+PKG = os.path.dirname(os.path.abspath(lla.__file__))
+
+
+def without_binding(tmp_path, code, garbage=False):
+    """Runs code on a copy of the package whose binding is missing, or not a library."""
+    to = tmp_path / "looped_transformer_decode_b200"
+    to.mkdir()
+    for name in os.listdir(PKG):
+        if name.endswith((".py", "liblla.so")):
+            shutil.copy(os.path.join(PKG, name), to / name)
+    if garbage:
+        (to / "_binding.so").write_bytes(b"not a library")
+    return subprocess.run([sys.executable, "-c", code], cwd=tmp_path, capture_output=True, text=True,
+                          timeout=600, env={**os.environ, "PYTHONPATH": str(tmp_path)})
+
+
+CODE = """
+import torch, looped_transformer_decode_b200 as lla
+assert lla.__file__.startswith({where!r}), lla.__file__
+cfg = lla.Cfg(4, 2, 64, 16, 32)
+assert lla.ratio(cfg) == lla.Fraction(32, 3)
+assert lla.decode_launches(cfg, 2, 100) > 0 and lla.q8_decode_launches(cfg, 1, 64) == 1
+one = torch.zeros(1, dtype=torch.int32)
+try:
+    lla.page_map(16, one, one, one.view(1, 1), one, one, 4)
+except ImportError as e:
+    assert "page_map" in str(e) and "build" in str(e), e
+else:
+    raise SystemExit("no error")
+"""
+
+
+def test_package_imports_without_the_binding(tmp_path):
+    for garbage in (False, True):
+        where = tmp_path / str(garbage)
+        where.mkdir()
+        r = without_binding(where, CODE.format(where=str(where)), garbage)
+        assert r.returncode == 0, r.stdout + r.stderr
