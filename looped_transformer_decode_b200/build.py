@@ -11,6 +11,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblla.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_FOR = os.path.join(BUILD, "binding.txt")    # what _binding.so was built for, and how
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(ROOT, "include")]
@@ -67,9 +69,6 @@ def build_binding(verbose: bool = False, force: bool = False) -> str:
 
     src = os.path.join(CSRC, "binding.cpp")
     header = os.path.join(ROOT, "include", "lla.h")
-    if (not force and os.path.exists(BINDING)
-            and os.path.getmtime(BINDING) >= max(os.path.getmtime(src), os.path.getmtime(header))):
-        return BINDING
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     dirs = [os.path.join(ROOT, "include"), *include_paths(), os.path.join(cuda, "include"),
             sysconfig.get_paths()["include"]]
@@ -79,9 +78,21 @@ def build_binding(verbose: bool = False, force: bool = False) -> str:
            "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-L" + PKG,
            "-Wl,-rpath,$ORIGIN", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
            "-lc10", "-lc10_cuda", "-l:liblla.so"]
+    # it holds for one torch and one Python only
+    made_for = "\n".join([torch.__version__, sys.version, *cmd])
+    if not force and os.path.exists(BINDING) and os.path.exists(BINDING_FOR):
+        with open(BINDING_FOR) as f:
+            same = f.read() == made_for
+        if same and os.path.getmtime(BINDING) >= _newest([src, header]):
+            return BINDING
     if verbose:
         print(" ".join(cmd))
+    if os.path.exists(BINDING_FOR):
+        os.remove(BINDING_FOR)
     subprocess.run(cmd, check=True)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(BINDING_FOR, "w") as f:
+        f.write(made_for)
     return BINDING
 
 

@@ -6,7 +6,11 @@ import shutil
 import subprocess
 import sys
 
+import pytest
+import torch
+
 import looped_transformer_decode_b200 as lla
+from looped_transformer_decode_b200 import build as B
 
 PKG = os.path.dirname(os.path.abspath(lla.__file__))
 
@@ -46,3 +50,50 @@ def test_package_imports_without_the_binding(tmp_path):
         where.mkdir()
         r = without_binding(where, CODE.format(where=str(where)), garbage)
         assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.fixture
+def builds(tmp_path, monkeypatch):
+    """The build with outputs of its own and a compiler that only counts: a list of its commands."""
+    ran = []
+    monkeypatch.setattr(B, "BUILD", str(tmp_path))
+    monkeypatch.setattr(B, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(B, "BINDING_FOR", str(tmp_path / "binding.txt"))
+
+    def run(cmd, check):
+        ran.append(cmd)
+        (tmp_path / "_binding.so").write_bytes(b"")
+
+    monkeypatch.setattr(B.subprocess, "run", run)
+    return ran
+
+
+def test_binding_is_built_anew_for_another_torch_or_python(builds, monkeypatch):
+    B.build_binding()
+    B.build_binding()
+    assert len(builds) == 1
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    B.build_binding()
+    B.build_binding()
+    assert len(builds) == 2
+    monkeypatch.setattr(B.sys, "version", "2.7")
+    B.build_binding()
+    B.build_binding()
+    assert len(builds) == 3
+    os.remove(B.BINDING_FOR)                     # not known what it was built for
+    B.build_binding()
+    assert len(builds) == 4
+    B.build_binding(force=True)
+    assert len(builds) == 5
+
+
+def test_a_failed_build_leaves_no_mark(builds, monkeypatch):
+    B.build_binding()
+
+    def fail(cmd, check):
+        raise subprocess.CalledProcessError(1, cmd)
+
+    monkeypatch.setattr(B.subprocess, "run", fail)
+    with pytest.raises(subprocess.CalledProcessError):
+        B.build_binding(force=True)
+    assert not os.path.exists(B.BINDING_FOR)
