@@ -66,7 +66,7 @@ __device__ __forceinline__ bool append_unit(const Q8AppendArgs& a, int u, bool t
     return false;
   }
   const int first_row = a.row_start ? __ldg(a.row_start + lo) : s;
-  if (first_row < 0 || first_row > a.n_tok - (e - s)) {
+  if (e > s && (first_row < 0 || first_row > a.n_tok - (e - s))) {
     if (tell && a.status) atomicOr(a.status, LLA_STATUS_CTX_RANGE);
     return false;
   }

@@ -157,5 +157,12 @@ def test_rows_outside_are_skipped_and_told(n):
     assert torch.equal(cache.k[:width], whole.k[2 * width:])
     assert torch.equal(cache.k[width:2 * width], whole.k[:width])
     assert torch.equal(cache.k[2 * width:], whole.k[:width])
+    # a sequence without new tokens has no rows, and its entry is not looked at
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = lla.q8_cache_alloc(cfg, 3 * width, page)
+    lla.q8_append(cfg, None, cache, i32([n] * 3), bt, i32([0, n, n, 2 * n]), None, x, x,
+                  row_start=i32([0, -7, 2 * n]), status=status)
+    assert int(status) == 0 and not cache.k[width:2 * width].any()
+    assert torch.equal(cache.k[2 * width:], whole.k[2 * width:])
     with pytest.raises(ValueError, match="row_start"):
         lla.q8_append(cfg, None, cache, *args, row_start=i32([0, 1]))
