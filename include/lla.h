@@ -387,8 +387,9 @@ int lla_full_decode_attn(const lla_cfg* cfg, const void* rope_table, int32_t rop
  *           pair max(floor(at(beta_fast)), 0) to 1 at min(ceil(at(beta_slow)), rd - 1),
  *           at(n) = rd ln(orig_len / (2 pi n)) / (2 ln rope_base), the pair that turns n
  *           times over the orig_len positions trained on.
- * The tables stay plain rotations: the attention factor that goes with YARN
- * ((0.1 ln s + 1)^2 on the scores of whole-head RoPE) belongs in lla_cfg.sm_scale.
+ * The tables stay plain rotations: the attention factor that goes with YARN,
+ * f = (0.1 ln s + 1)^2 on the rotary dims' part of a score, belongs in lla_cfg.sm_scale where the
+ * whole head rotates; where only d_rope dims do, multiply those dims of the queries by f.
  */
 #define LLA_ROPE_SCALE_NONE 0
 #define LLA_ROPE_SCALE_LINEAR 1
@@ -555,8 +556,8 @@ int lla_q8_read(const lla_cfg* cfg, const lla_q8_cache* cache, int64_t n_rows,
                 void* stream);
 
 /* Workspace bytes of lla_q8_decode_attn for sequences of up to n_cap tokens (zero-filled
- * once before first use; its first two int32 words are the status words described at
- * lla_decode_workspace_bytes); 0 if the arguments are invalid. */
+ * once before first use); 0 if the arguments are invalid.  Its int32 word 1 holds the final
+ * status bits of the last completed call, as at lla_decode_workspace_bytes; word 0 is not used. */
 size_t lla_q8_decode_workspace_bytes(const lla_cfg* cfg, int32_t B, int32_t n_cap);
 
 /* Kernel launches one lla_q8_decode_attn call makes, or -1 if invalid. */

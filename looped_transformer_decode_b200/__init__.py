@@ -12,8 +12,8 @@ from fractions import Fraction
 
 import torch
 
-from ._lib import (BF16, ERR_CUDA, ERR_INVALID, ERR_TOO_SMALL, ERR_UNSUPPORTED, F32, LIB_PATH,
-                   MODE_2D, MODE_PER_HEAD, OK, ROPE_LAYOUTS, SIGNATURES, STATUS_CTX_RANGE,
+from ._lib import (ERR_CUDA, ERR_INVALID, ERR_TOO_SMALL, ERR_UNSUPPORTED, LIB_PATH, MODE_2D,
+                   MODE_PER_HEAD, OK, SIGNATURES, STATUS_CTX_RANGE,
                    STATUS_NONFINITE, STATUS_PAGE_RANGE, STATUS_PAGES_SHORT, STATUS_POSITION_RANGE,
                    STATUS_ROPE_TABLE, STATUS_SLOT_RANGE, STATUS_TIMEOUT, Cfg, CQ8Cache, LLAError, RopeScaling, check,
                    last_error, lib)
@@ -296,7 +296,8 @@ def rope_apply(cfg: Cfg, rope, positions, x, layout: str = "half", inverse: bool
 
     Rotary dims as ``cfg`` has them, pairs by ``layout`` ("half" or "interleaved").  Tokens may be
     strided (a slice of a fused projection); ``out`` may be ``x``.  ``inverse=True`` rotates back,
-    which is the gradient with respect to x given the gradient of the output.
+    which is the gradient with respect to x given the gradient of the output; no autograd graph is
+    recorded, so call it from a backward of your own.
     """
     return _binding.rope_apply(cfg, rope, positions, x, layout, inverse, out, status)
 
@@ -385,8 +386,9 @@ def q8_decode_attn(cfg: Cfg, rope, cache: Q8Cache, ctx_len, block_table, q, k_se
     """Decode attention over the 8-bit cache; returns out [B, H, d] of q's dtype.
 
     ``q``, ``k_self``, ``v_self`` fp32 or bf16 [B, H, d] before rotation (rotated already with
-    ``rope=None``); ``k_self=v_self=None`` attends over the history alone.  Calls that may run at
-    the same time need a workspace each.
+    ``rope=None``), contiguous; ``k_self=v_self=None`` attends over the history alone.  Calls that
+    may run at the same time need a workspace each; decode_status reads a call's status from its
+    workspace, and without ``ws`` there is none to read.
     """
     return _binding.q8_decode_attn(cfg, rope, cache, ctx_len, block_table, q, k_self, v_self, q_pos,
                                    layout, out, ws)

@@ -26,9 +26,7 @@ STATUS_PAGES_SHORT = 32
 STATUS_NONFINITE = 64
 STATUS_ROPE_TABLE = 128
 
-ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALES = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-F32, BF16 = 0, 1
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_TOO_SMALL, ERR_CUDA = 0, -1, -2, -3, -4
 

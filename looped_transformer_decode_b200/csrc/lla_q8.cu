@@ -1,5 +1,5 @@
-// Paged 8-bit cache of exact keys and values: the append that quantises, the read
-// that gives rows back, and decode attention.
+// Paged 8-bit cache of exact keys and values: the append that quantises and the read
+// that gives rows back (decode attention: lla_q8_decode.cu).
 //
 // A page holds P tokens of one sequence; per head its keys (rotated) and its values
 // are P x d int8 codes with one fp32 scale each, value = code * scale.  Layout
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) q8_append_kernel(Q8AppendAr
 // team holds a full page of its head in registers, rotated, between its largest magnitude and
 // its codes.  The rows of the next groups are on their way meanwhile, into a ring in shared
 // memory of which every thread fills and reads its own part, so that nothing waits for it but
-// the thread itself.  20011 tokens of 16 heads of 128: bf16 68 us, fp32 83 (their bytes take 38
+// the thread itself.  20011 tokens of 16 heads of 128: bf16 67 us, fp32 83 (their bytes take 38
 // and 63 at the copy rate); without the ring and with a block per page and four heads 128.
 template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? kAppendBlocksPerSm : 1)

@@ -128,10 +128,6 @@ __device__ __forceinline__ void load_words(const unsigned char* p, uint32_t* w) 
     w[1] = u.y;
     w[2] = u.z;
     w[3] = u.w;
-  } else if constexpr (W == 2) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    w[0] = u.x;
-    w[1] = u.y;
   } else {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
