@@ -44,9 +44,10 @@ struct Q8Shape {
   // four of them are a group, the unit of the arithmetic.  kSubs 16-token blocks, each in
   // one page, make a group; two groups make a tile.
   static constexpr int kLanes = D == 96 ? 8 : D / 16;
-  // Registers bound the blocks per SM: two take 180 a thread, three of 168 fit without spills but
-  // divide middling batches worse (16 heads of 128; 64 x 512 tokens 30 us against 37, 256 x 4096
-  // 642 against 657, 1024 x 64 88 against 74).  Lanes of 96 hold 12 codes and need fewer.
+  // Registers bound the blocks per SM: two take 180 a thread; three of 168 fit without spills and
+  // are better for some sizes and worse for others (16 heads of 128, us with two against three:
+  // 64 x 512 tokens 30 and 37, 1024 x 64 88 and 74, 128 x 1000 97 and 93, 256 x 4096 633 and 651,
+  // repeated under the power limit 761 and 720).  Lanes of 96 hold 12 codes and need fewer.
   static constexpr int kBlocksPerSm = D == 96 ? 3 : 2;
   static constexpr int kWords = D / kLanes / 4;             // 4-code words per lane and row
   static constexpr int kRows = 32 / kLanes;

@@ -133,7 +133,7 @@ cudaError_t launch_rope_t(RopeApplyArgs a, cudaStream_t s) {
   constexpr int kHeads = 4;
   const int tpr = a.d / kChunkDims<T>;
   // Four heads a thread where that leaves two blocks per SM: 32768 bf16 tokens of 16 heads of
-  // 128, half of each rotated, 47.6 us (89% of the copy rate); small calls want the threads.
+  // 128, half of each rotated, 48.4 us (87% of the copy rate); small calls want the threads.
   const bool many = a.n_tok * a.n_heads * tpr >= (long long)kHeads * kRopeThreads * 2 * sm_count();
   a.groups = many ? (a.n_heads + kHeads - 1) / kHeads : a.n_heads;
   const int per_tok = a.groups * tpr;
