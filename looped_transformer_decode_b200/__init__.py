@@ -172,10 +172,10 @@ def decode_attn(cfg: Cfg, packed, rope, t: int, ctx_len, q, k_self, v_self, posi
     n_cap = positions.shape[1]
     if H != cfg.H or d != cfg.d_head:
         raise ValueError("q shape does not match cfg")
-    for table in (rope, rope._base):
-        if getattr(table, "scaled_frequencies", False):
-            raise ValueError("rope has scaled frequencies: decode_attn forms the history's angles "
-                             "from cfg.rope_base")
+    table = rope if hasattr(rope, "scaled_frequencies") else getattr(rope, "_base", None)
+    if getattr(table, "scaled_frequencies", False):
+        raise ValueError("rope has scaled frequencies: decode_attn forms the history's angles "
+                         "from cfg.rope_base")
     if out is None:
         out = torch.empty((B, H, d), dtype=torch.float32, device=q.device)
     if ws is None:

@@ -25,6 +25,14 @@ def test_python_call_refuses_a_marked_table():
     for t in (table, table[:4]):
         with pytest.raises(ValueError, match="scaled frequencies"):
             lla.decode_attn(cfg, None, t, 0, one[0], x, x, x, one, one[0], None, None)
+    part = table[:4]
+    part.scaled_frequencies = False              # as after rope_table(out=part)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        lla.decode_attn(cfg, x.byte(), part, 0, one[0], x, x, x, one, one[0], None, None,
+                        ws=torch.zeros(8, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="rope must be|packed must be"):
+        lla.decode_attn(cfg, None, None, 0, one[0], x, x, x, one, one[0], None, None,
+                        ws=torch.zeros(8, dtype=torch.uint8))
 
 
 @pytest.mark.gpu
