@@ -576,7 +576,7 @@ int lla_q8_decode_launches(const lla_cfg* cfg, int32_t B, int32_t n_cap);
  * holds past ctx_len[b] or in pages of other sequences does not reach the output.
  * Softmax, weights and sums are held in fp32.  A score is an exact integer dot product per 16
  * dims (12 with d_head 96), in which each element of q is held to 2^-24 of the largest of
- * those dims, times fp32 scales.
+ * those dims (at or below 1e-30 they count as zeros), times fp32 scales.
  * B <= 65535; B * H * (max_pages * page / 32 + 16) at most 2^31 - 4097 (LLA_ERR_UNSUPPORTED).
  */
 int lla_q8_decode_attn(const lla_cfg* cfg, const lla_q8_cache* cache, const void* rope_table,
